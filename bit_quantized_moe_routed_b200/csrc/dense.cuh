@@ -1,0 +1,70 @@
+// dense.cuh -- what the kernels of the dense operators (quant_i8.cu,
+// dense_*.cu) and their entry points (dense_api.cu) share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+
+namespace moeq {
+namespace dense {
+
+// What a product kernel does with its sums.
+enum Epi : int {
+    EPI_STORE = 0,    // out = acc (scaled for int8)
+    EPI_GLU = 1,      // out = silu(acc0) acc1; keep[0/1] = acc0 / acc1 where given
+    EPI_GLU_BWD = 2   // keep[0/1] = gradients of acc0 / acc1 for the gradient dh of silu(acc0) acc1
+};
+
+// out[z] = sum over segments s of A_s B_s^T, or with two B (EPI_GLU*) both
+// products of one A.  All strides in elements.
+struct Product {
+    // rows of A (M) and of B (N), reduction length of one segment
+    long long M = 0, N = 0, K = 0;
+    int nseg = 1;     // segments along the reduction (dx: gate, then up)
+    int nbatch = 1;   // independent products of one B (dW: gate, up)
+    const void *a[2] = {nullptr, nullptr};   // per segment, or per batch
+    long long ald = 0;
+    bool a_t = false;                        // A is stored [K][M]
+    const void *b[2] = {nullptr, nullptr};   // per segment, or gate / up
+    long long bld[2] = {0, 0};
+    bool b_t = false;                        // B is stored [K][N]
+    const float *a_scale = nullptr;          // int8: [M]
+    const float *b_scale[2] = {nullptr, nullptr};   // int8: [N]
+    void *out[2] = {nullptr, nullptr};       // per batch
+    long long old[2] = {0, 0};
+    void *keep[2] = {nullptr, nullptr};      // [M][N] planes, row stride kld
+    long long kld = 0;
+    const void *dh = nullptr;                // [M][N], row stride dhld (EPI_GLU_BWD)
+    long long dhld = 0;
+    int in_dtype = MOEQ_ACT_F32;             // moeq_dtype, or kI8
+    int out_dtype = MOEQ_ACT_F32;            // of out, keep and dh
+    int epi = EPI_STORE;
+};
+constexpr int kI8 = 100;
+
+// silu and its derivative from the sigmoid s = 1 / (1 + e^-g)
+__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+__device__ __forceinline__ void glu_grad(float g, float u, float dh, float &dg, float &du) {
+    const float s = sigmoid_f32(g);
+    dg = dh * u * (s * (1.0f + g * (1.0f - s)));
+    du = dh * (g * s);
+}
+
+__device__ __forceinline__ float ld_elem(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float ld_elem(const __nv_bfloat16 *p) {
+    return bf16_bits_to_f32(__ldg(reinterpret_cast<const unsigned short *>(p)));
+}
+__device__ __forceinline__ void st_elem(float *p, float v) { *p = v; }
+__device__ __forceinline__ void st_elem(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// ---- launchers ----
+cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
+// dgu[0/1] (row stride ld) = the gradients of the kept projections gu [2][M][N]
+cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,
+                             long long M, long long N, int dtype, cudaStream_t s);
+
+}  // namespace dense
+}  // namespace moeq

@@ -1,0 +1,311 @@
+// dense_api.cu -- entry points of the dense operators: argument checks, the
+// workspace's layout and the choice of kernels.  See include/moeq.h for what
+// each call computes.
+#include <algorithm>
+#include <mutex>
+
+#include "dense.cuh"
+
+namespace moeq {
+
+cudaError_t launch_quant_i8(const void *x, int dtype, int rows, int cols, long long ldx, int8_t *q, long long ldq,
+                            float *scale, cudaStream_t s);
+
+namespace dense {
+namespace {
+
+constexpr long long kMaxDim = 1LL << 21;      // hidden, inter, n_in, n_out
+constexpr long long kMaxLd = 1LL << 36;
+constexpr int kMaxI8K = 131071;               // 2^14 K < 2^31
+
+bool known_dtype(int d) { return d == MOEQ_ACT_F32 || d == MOEQ_ACT_BF16; }
+int elem_size(int d) { return d == MOEQ_ACT_F32 ? 4 : (d == MOEQ_ACT_BF16 ? 2 : 1); }
+
+// A rows x cols array with row stride ld, in bytes.
+struct Span {
+    uintptr_t p = 0;
+    unsigned long long row = 0, ld = 0, rows = 0;
+    Span() {}
+    Span(const void *q, long long rows_, long long cols, long long ld_, int es)
+        : p((uintptr_t)q), row((unsigned long long)cols * es), ld((unsigned long long)ld_ * es),
+          rows((unsigned long long)rows_) {}
+    bool empty() const { return !p || !rows || !row; }
+    uintptr_t end() const { return p + (rows - 1) * ld + row; }
+};
+// Whether two arrays share a byte.  Arrays of one row stride whose column
+// windows are disjoint (slices of one buffer) do not.
+bool overlap(const Span &a, const Span &b) {
+    if (a.empty() || b.empty() || a.end() <= b.p || b.end() <= a.p) return false;
+    if (a.ld == b.ld && a.rows > 1 && b.rows > 1) {
+        const unsigned long long d = a.p <= b.p ? (b.p - a.p) % a.ld : a.ld - 1 - ((a.p - b.p - 1) % a.ld);
+        return d < a.row || d + b.row > a.ld;
+    }
+    return true;
+}
+template <int N, int M>
+bool any_overlap(const Span (&outs)[N], const Span (&ins)[M]) {
+    for (int i = 0; i < N; ++i) {
+        for (int j = 0; j < M; ++j)
+            if (overlap(outs[i], ins[j])) return true;
+        for (int j = i + 1; j < N; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+bool matrix_ok(const void *p, long long cols, long long ld, int es) {
+    return p && ld >= cols && ld <= kMaxLd && !((uintptr_t)p % es);
+}
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+moeq_status done(cudaError_t e) { return e == cudaSuccess ? MOEQ_OK : MOEQ_ERR_CUDA; }
+
+// Sizes of the workspace's parts, in the order they lie in it.
+struct Plan {
+    size_t dgu = 0;            // gradients of the projections, [2][T][dgu_ld]
+    long long dgu_ld = 0;
+    size_t total() const { return dgu; }
+};
+
+bool i8_args_ok(const moeq_i8_args *a, int nw) {
+    if (!a || (nw != 1 && nw != 2) || a->n_tokens < 0 || a->n_in < 1 || a->n_in > kMaxI8K || a->n_out < 1 ||
+        a->n_out > kMaxDim || !known_dtype(a->out_dtype))
+        return false;
+    const bool any = a->n_tokens > 0;   // the arrays of no tokens may be NULL
+    if (any && (!matrix_ok(a->x, a->n_in, a->ldx, 1) || !a->x_scale || ((uintptr_t)a->x_scale & 3u) ||
+                !matrix_ok(a->out, a->n_out, a->ldo, elem_size(a->out_dtype))))
+        return false;
+    for (int i = 0; i < nw; ++i)
+        if (!matrix_ok(a->w[i], a->n_in, a->ldw[i], 1) || !a->w_scale[i] || ((uintptr_t)a->w_scale[i] & 3u))
+            return false;
+    if (nw == 1 && (a->w[1] || a->ldw[1] || a->w_scale[1])) return false;
+    return true;
+}
+Plan plan_i8(const moeq_i8_args *, int) { return Plan(); }
+
+bool glu_args_ok(const moeq_glu_args *a, bool backward) {
+    if (!a || a->n_tokens < 0 || a->hidden < 1 || a->hidden > kMaxDim || a->inter < 1 || a->inter > kMaxDim ||
+        !known_dtype(a->dtype))
+        return false;
+    const int es = elem_size(a->dtype);
+    const bool any = a->n_tokens > 0;
+    if (any && !matrix_ok(a->x, a->hidden, a->ldx, es)) return false;
+    for (int i = 0; i < 2; ++i)
+        if (!matrix_ok(a->w[i], a->hidden, a->ldw[i], es)) return false;
+    if ((uintptr_t)a->gu % es) return false;
+    if (!backward) return !any || matrix_ok(a->h, a->inter, a->ldh, es);
+    if (any && !matrix_ok(a->dh, a->inter, a->lddh, es)) return false;
+    if ((a->dw[0] == nullptr) != (a->dw[1] == nullptr)) return false;
+    if (!a->dx && !a->dw[0] && any) return false;
+    if (a->dx && !matrix_ok(a->dx, a->hidden, a->lddx, es)) return false;
+    for (int i = 0; i < 2; ++i)
+        if (a->dw[i] && !matrix_ok(a->dw[i], a->hidden, a->lddw[i], es)) return false;
+    return true;
+}
+Plan plan_glu(const moeq_glu_args *a, bool backward) {
+    Plan p;
+    if (!backward || a->n_tokens == 0) return p;
+    p.dgu_ld = (a->inter + 63) / 64 * 64;
+    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * elem_size(a->dtype));
+    return p;
+}
+
+bool workspace_ok(const void *ws, long long bytes, const Plan &p) {
+    return p.total() == 0 || (ws && !((uintptr_t)ws & 255u) && bytes >= 0 && (size_t)bytes >= p.total());
+}
+
+moeq_status run_i8(const moeq_i8_args *a, int nw, cudaStream_t s) {
+    if (!i8_args_ok(a, nw)) return MOEQ_ERR_INVALID_ARGUMENT;
+    if (a->n_tokens == 0) return MOEQ_OK;
+    const Plan plan = plan_i8(a, nw);
+    if (!workspace_ok(a->workspace, a->workspace_bytes, plan)) return MOEQ_ERR_INVALID_ARGUMENT;
+    const long long T = a->n_tokens, N = a->n_out, K = a->n_in;
+    const Span outs[2] = {Span(a->out, T, N, a->ldo, elem_size(a->out_dtype)),
+                          Span(a->workspace, 1, (long long)plan.total(), (long long)plan.total(), 1)};
+    const Span ins[6] = {Span(a->x, T, K, a->ldx, 1),         Span(a->w[0], N, K, a->ldw[0], 1),
+                         Span(a->w[1], N, K, a->ldw[1], 1),   Span(a->x_scale, 1, T, T, 4),
+                         Span(a->w_scale[0], 1, N, N, 4),     Span(a->w_scale[1], 1, N, N, 4)};
+    if (any_overlap(outs, ins)) return MOEQ_ERR_INVALID_ARGUMENT;
+    Product p;
+    p.M = T;
+    p.N = N;
+    p.K = K;
+    p.a[0] = a->x;
+    p.ald = a->ldx;
+    p.a_scale = a->x_scale;
+    for (int i = 0; i < nw; ++i) {
+        p.b[i] = a->w[i];
+        p.bld[i] = a->ldw[i];
+        p.b_scale[i] = a->w_scale[i];
+    }
+    p.out[0] = a->out;
+    p.old[0] = a->ldo;
+    p.in_dtype = kI8;
+    p.out_dtype = a->out_dtype;
+    p.epi = nw == 2 ? EPI_GLU : EPI_STORE;
+    return done(launch_product_simt(p, s));
+}
+
+}  // namespace
+}  // namespace dense
+}  // namespace moeq
+
+using namespace moeq;
+using namespace moeq::dense;
+
+extern "C" moeq_status moeq_quant_i8(const void *x, int32_t dtype, int32_t n_rows, int32_t n_cols, int64_t ldx,
+                                     int8_t *q, int64_t ldq, float *scale, void *stream) {
+    if (!known_dtype(dtype) || n_rows < 0 || n_cols < 1) return MOEQ_ERR_INVALID_ARGUMENT;
+    if (n_rows == 0) return MOEQ_OK;
+    const int es = elem_size(dtype);
+    if (!matrix_ok(x, n_cols, ldx, es) || !matrix_ok(q, n_cols, ldq, 1) || !scale || ((uintptr_t)scale & 3u))
+        return MOEQ_ERR_INVALID_ARGUMENT;
+    const Span outs[2] = {Span(q, n_rows, n_cols, ldq, 1), Span(scale, 1, n_rows, n_rows, 4)};
+    const Span ins[1] = {Span(x, n_rows, n_cols, ldx, es)};
+    if (any_overlap(outs, ins)) return MOEQ_ERR_INVALID_ARGUMENT;
+    return done(launch_quant_i8(x, dtype, n_rows, n_cols, ldx, q, ldq, scale, (cudaStream_t)stream));
+}
+
+extern "C" moeq_status moeq_matmul_i8(const moeq_i8_args *a, void *stream) {
+    return run_i8(a, 1, (cudaStream_t)stream);
+}
+extern "C" moeq_status moeq_glu_i8(const moeq_i8_args *a, void *stream) { return run_i8(a, 2, (cudaStream_t)stream); }
+extern "C" int64_t moeq_i8_workspace(const moeq_i8_args *a, int32_t n_w) {
+    return i8_args_ok(a, n_w) ? (int64_t)plan_i8(a, n_w).total() : -1;
+}
+
+extern "C" int64_t moeq_glu_workspace(const moeq_glu_args *a, int32_t backward) {
+    if ((backward != 0 && backward != 1) || !glu_args_ok(a, backward == 1)) return -1;
+    return (int64_t)plan_glu(a, backward == 1).total();
+}
+
+extern "C" moeq_status moeq_glu(const moeq_glu_args *a, void *stream) {
+    if (!glu_args_ok(a, false)) return MOEQ_ERR_INVALID_ARGUMENT;
+    if (a->n_tokens == 0) return MOEQ_OK;
+    const Plan plan = plan_glu(a, false);
+    if (!workspace_ok(a->workspace, a->workspace_bytes, plan)) return MOEQ_ERR_INVALID_ARGUMENT;
+    const long long T = a->n_tokens, H = a->hidden, I = a->inter;
+    const int es = elem_size(a->dtype);
+    const Span outs[3] = {Span(a->h, T, I, a->ldh, es), Span(a->gu, 2 * T, I, I, es),
+                          Span(a->workspace, 1, (long long)plan.total(), (long long)plan.total(), 1)};
+    const Span ins[3] = {Span(a->x, T, H, a->ldx, es), Span(a->w[0], I, H, a->ldw[0], es),
+                         Span(a->w[1], I, H, a->ldw[1], es)};
+    if (any_overlap(outs, ins)) return MOEQ_ERR_INVALID_ARGUMENT;
+    Product p;
+    p.M = T;
+    p.N = I;
+    p.K = H;
+    p.a[0] = a->x;
+    p.ald = a->ldx;
+    for (int i = 0; i < 2; ++i) {
+        p.b[i] = a->w[i];
+        p.bld[i] = a->ldw[i];
+        if (a->gu) p.keep[i] = (char *)a->gu + (size_t)i * T * I * es;
+    }
+    p.kld = I;
+    p.out[0] = a->h;
+    p.old[0] = a->ldh;
+    p.in_dtype = p.out_dtype = a->dtype;
+    p.epi = EPI_GLU;
+    return done(launch_product_simt(p, (cudaStream_t)stream));
+}
+
+extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
+    if (!glu_args_ok(a, true)) return MOEQ_ERR_INVALID_ARGUMENT;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const long long T = a->n_tokens, H = a->hidden, I = a->inter;
+    const int es = elem_size(a->dtype);
+    const Plan plan = plan_glu(a, true);
+    if (!workspace_ok(a->workspace, a->workspace_bytes, plan)) return MOEQ_ERR_INVALID_ARGUMENT;
+    const Span outs[4] = {Span(a->dx, T, H, a->lddx, es), Span(a->dw[0], I, H, a->lddw[0], es),
+                          Span(a->dw[1], I, H, a->lddw[1], es),
+                          Span(a->workspace, 1, (long long)plan.total(), (long long)plan.total(), 1)};
+    const Span ins[5] = {Span(a->x, T, H, a->ldx, es), Span(a->w[0], I, H, a->ldw[0], es),
+                         Span(a->w[1], I, H, a->ldw[1], es), Span(a->gu, 2 * T, I, I, es),
+                         Span(a->dh, T, I, a->lddh, es)};
+    if (any_overlap(outs, ins)) return MOEQ_ERR_INVALID_ARGUMENT;
+    if (T == 0) {
+        for (int i = 0; i < 2 && a->dw[i]; ++i) {
+            const cudaError_t e = cudaMemset2DAsync(a->dw[i], (size_t)a->lddw[i] * es, 0, (size_t)H * es, (size_t)I, s);
+            if (e != cudaSuccess) return MOEQ_ERR_CUDA;
+        }
+        return MOEQ_OK;
+    }
+    char *dg = (char *)a->workspace, *du = dg + (size_t)T * plan.dgu_ld * es;
+    cudaError_t e;
+    if (a->gu) {
+        e = launch_glu_dgate(a->dh, a->lddh, a->gu, dg, du, plan.dgu_ld, T, I, a->dtype, s);
+    } else {
+        Product p;
+        p.M = T;
+        p.N = I;
+        p.K = H;
+        p.a[0] = a->x;
+        p.ald = a->ldx;
+        for (int i = 0; i < 2; ++i) {
+            p.b[i] = a->w[i];
+            p.bld[i] = a->ldw[i];
+        }
+        p.keep[0] = dg;
+        p.keep[1] = du;
+        p.kld = plan.dgu_ld;
+        p.dh = a->dh;
+        p.dhld = a->lddh;
+        p.in_dtype = p.out_dtype = a->dtype;
+        p.epi = EPI_GLU_BWD;
+        e = launch_product_simt(p, s);
+    }
+    if (e == cudaSuccess && a->dx) {
+        Product p;   // dx = dg W_gate + du W_up: two segments along the reduction
+        p.M = T;
+        p.N = H;
+        p.K = I;
+        p.nseg = 2;
+        p.a[0] = dg;
+        p.a[1] = du;
+        p.ald = plan.dgu_ld;
+        p.b_t = true;
+        for (int i = 0; i < 2; ++i) {
+            p.b[i] = a->w[i];
+            p.bld[i] = a->ldw[i];
+        }
+        p.out[0] = a->dx;
+        p.old[0] = a->lddx;
+        p.in_dtype = p.out_dtype = a->dtype;
+        e = launch_product_simt(p, s);
+    }
+    if (e == cudaSuccess && a->dw[0]) {
+        Product p;   // dW_i = d_i^T x: two products of one B
+        p.M = I;
+        p.N = H;
+        p.K = T;
+        p.nbatch = 2;
+        p.a[0] = dg;
+        p.a[1] = du;
+        p.ald = plan.dgu_ld;
+        p.a_t = p.b_t = true;
+        p.b[0] = a->x;
+        p.bld[0] = a->ldx;
+        for (int i = 0; i < 2; ++i) {
+            p.out[i] = a->dw[i];
+            p.old[i] = a->lddw[i];
+        }
+        p.in_dtype = p.out_dtype = a->dtype;
+        e = launch_product_simt(p, s);
+    }
+    return done(e);
+}
+
+namespace {
+__device__ uint32_t g_dense_status;
+}
+
+extern "C" moeq_status moeq_dense_status(int32_t clear) {
+    if (cudaDeviceSynchronize() != cudaSuccess) return MOEQ_ERR_CUDA;
+    uint32_t w = 0;
+    if (cudaMemcpyFromSymbol(&w, g_dense_status, sizeof(w)) != cudaSuccess) return MOEQ_ERR_CUDA;
+    if (clear && w) {
+        const uint32_t zero = 0;
+        if (cudaMemcpyToSymbol(g_dense_status, &zero, sizeof(zero)) != cudaSuccess) return MOEQ_ERR_CUDA;
+    }
+    return w ? MOEQ_ERR_TIMEOUT : MOEQ_OK;
+}

@@ -8,7 +8,9 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
+import struct
 
 import numpy as np
 
@@ -31,7 +33,9 @@ GATE, UP, DOWN = 0, 1, 2
 EXPORTS = ("moeq_layer_create", "moeq_upload_weights", "moeq_forward", "moeq_forward_host",
            "moeq_forward_profiled", "moeq_route", "moeq_dequant", "moeq_layer_status",
            "moeq_status_string", "moeq_layer_destroy", "moeq_kernel_launches", "moeq_route_noalloc",
-           "moeq_router_upload", "moeq_router", "moeq_forward_routed", "moeq_vq_encode")
+           "moeq_router_upload", "moeq_router", "moeq_forward_routed", "moeq_vq_encode",
+           "moeq_quant_i8", "moeq_matmul_i8", "moeq_glu_i8", "moeq_i8_workspace", "moeq_glu",
+           "moeq_glu_backward", "moeq_glu_workspace", "moeq_dense_status")
 SCORE = {"sigmoid": 0, "softmax": 1}
 
 
@@ -74,6 +78,22 @@ _lib.moeq_kernel_launches.restype = C.c_int64
 for _f in ("moeq_layer_create", "moeq_upload_weights", "moeq_forward", "moeq_forward_host", "moeq_dequant",
            "moeq_layer_status", "moeq_forward_profiled", "moeq_route", "moeq_route_noalloc",
            "moeq_router_upload", "moeq_router", "moeq_forward_routed", "moeq_vq_encode"):
+    getattr(_lib, _f).restype = C.c_int
+
+
+# the argument structs of the dense operators, packed as the C compiler lays
+# them out (native sizes and alignment)
+I8_ARGS = struct.Struct("@4i Pq P 2P 2q 2P Pq Pq")      # moeq_i8_args
+GLU_ARGS = struct.Struct("@4i Pq 2P 2q P Pq Pq Pq 2P 2q Pq")   # moeq_glu_args
+_lib.moeq_quant_i8.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_void_p, C.c_int64,
+                               C.c_void_p, C.c_void_p]
+for _f in ("moeq_matmul_i8", "moeq_glu_i8", "moeq_glu", "moeq_glu_backward"):
+    getattr(_lib, _f).argtypes = [C.c_char_p, C.c_void_p]
+for _f in ("moeq_i8_workspace", "moeq_glu_workspace"):
+    getattr(_lib, _f).argtypes = [C.c_char_p, C.c_int32]
+    getattr(_lib, _f).restype = C.c_int64
+_lib.moeq_dense_status.argtypes = [C.c_int32]
+for _f in ("moeq_quant_i8", "moeq_matmul_i8", "moeq_glu_i8", "moeq_glu", "moeq_glu_backward", "moeq_dense_status"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -136,6 +156,198 @@ def vq_encode(w, book13, book8=None, gain=None, col_weight=None, stream=None):
     _check(_lib.moeq_vq_encode(p(w), N, K, p(gain), p(col_weight), p(book13), p(book8), p(idx13), p(idx8),
                                _stream_ptr(stream)), "moeq_vq_encode")
     return idx13, idx8
+
+
+def _need(cond, what):
+    if not cond:
+        raise MoeqError(INVALID_ARGUMENT, what)
+
+
+def _act(t, what):
+    """moeq_dtype of a tensor."""
+    import torch
+    if t.dtype is torch.bfloat16:
+        return 1
+    _need(t.dtype is torch.float32, f"{what}: dtype {t.dtype}")
+    return 0
+
+
+def _ld(t, shape, dtype, dev, what):
+    """Row stride of a 2-D cuda tensor with unit column stride, checked
+    against the shape, dtype and device it must have."""
+    _need(t.is_cuda and t.get_device() == dev and t.dtype is dtype and tuple(t.shape) == tuple(shape),
+          f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, need {dtype} {tuple(shape)} on cuda:{dev}")
+    rs, cs = t.stride()
+    _need(cs == 1 or t.shape[1] <= 1, f"{what}: column stride {cs}")
+    return max(rs, shape[1]) if shape[0] <= 1 else rs
+
+
+def _vec(t, n, dev, what):
+    import torch
+    _need(t.is_cuda and t.get_device() == dev and t.dtype is torch.float32 and tuple(t.shape) == (n,)
+          and t.is_contiguous(), f"{what}: need contiguous float32 ({n},) on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _on_stream(fn):
+    """Run a dense operator's wrapper on ``stream``, or on the current stream
+    of its first tensor's device: allocations it makes belong to that stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        import torch
+        _need(isinstance(first, torch.Tensor) and first.is_cuda, f"{fn.__name__}: a cuda tensor is needed")
+        if stream is not None:
+            _need(stream.device == first.device, f"{fn.__name__}: stream on {stream.device}, tensor on {first.device}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, _s=stream.cuda_stream, **kw)
+        dev = first.get_device()
+        if torch.cuda.current_device() != dev:
+            with torch.cuda.device(dev):
+                return fn(first, *args, _s=torch.cuda.current_stream(dev).cuda_stream, **kw)
+        return fn(first, *args, _s=torch.cuda.current_stream(dev).cuda_stream, **kw)
+    return call
+
+
+def _call(name, ws_name, which, pack, workspace, dev, s):
+    """One call with its workspace: ``pack(pointer, bytes)`` gives the packed
+    arguments.  A missing workspace is allocated on the call's stream."""
+    import torch
+    args = pack(0, 0)
+    n = getattr(_lib, ws_name)(args, which)
+    _need(n >= 0, name)
+    if n:
+        if workspace is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
+        _need(workspace.is_cuda and workspace.get_device() == dev and workspace.is_contiguous()
+              and workspace.numel() * workspace.element_size() >= n,
+              f"{name}: workspace of {n} contiguous bytes on cuda:{dev}")
+        args = pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(getattr(_lib, name)(args, s), name)
+
+
+@_on_stream
+def quant_i8(x, q=None, scale=None, _s=0):
+    """moeq_quant_i8: rows of x (float32 or bfloat16 [M][K], unit column
+    stride) to (q int8 [M][K], scale float32 [M]), x ~ q * scale[:, None]."""
+    import torch
+    _need(x.dim() == 2, "quant_i8: x is not 2-D")
+    M, K = x.shape
+    dev = x.get_device()
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    ldx = _ld(x, (M, K), x.dtype, dev, "quant_i8: x")
+    _check(_lib.moeq_quant_i8(x.data_ptr(), _act(x, "quant_i8: x"), M, K, ldx, q.data_ptr(),
+                              _ld(q, (M, K), torch.int8, dev, "quant_i8: q"), _vec(scale, M, dev, "quant_i8: scale"),
+                              _s), "moeq_quant_i8")
+    return q, scale
+
+
+def _i8(name, n_w, xq, xs, ws, out, dtype, workspace, s):
+    import torch
+    _need(xq.dim() == 2 and ws[0][0].dim() == 2, f"{name}: operands are not 2-D")
+    T, K = xq.shape
+    N = ws[0][0].shape[0]
+    dev = xq.get_device()
+    if out is None:
+        _need(dtype in ACT, f"{name}: dtype {dtype!r}")
+        out = torch.empty((T, N), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device=xq.device)
+    act = _act(out, f"{name}: out")
+    ldx = _ld(xq, (T, K), torch.int8, dev, f"{name}: xq")
+    px = _vec(xs, T, dev, f"{name}: xs")
+    w, ld, sc = [0, 0], [0, 0], [0, 0]
+    for i, (wq, s_w) in enumerate(ws):
+        w[i], ld[i] = wq.data_ptr(), _ld(wq, (N, K), torch.int8, dev, f"{name}: weight {i}")
+        sc[i] = _vec(s_w, N, dev, f"{name}: weight scale {i}")
+    ldo = _ld(out, (T, N), out.dtype, dev, f"{name}: out")
+    head = (T, K, N, act, xq.data_ptr(), ldx, px, w[0], w[1], ld[0], ld[1], sc[0], sc[1], out.data_ptr(), ldo)
+    _call("moeq_" + name, "moeq_i8_workspace", n_w, lambda p, n: I8_ARGS.pack(*head, p, n), workspace, dev, s)
+    return out
+
+
+@_on_stream
+def matmul_i8(xq, xs, wq, ws, out=None, dtype="bf16", workspace=None, _s=0):
+    """moeq_matmul_i8: (xq wq^T) xs[:, None] ws with xq int8 [T][K], wq int8
+    [N][K], xs float32 [T], ws float32 [N]; [T][N] in ``dtype`` ("bf16" or
+    "f32"), or into ``out``."""
+    return _i8("matmul_i8", 1, xq, xs, [(wq, ws)], out, dtype, workspace, _s)
+
+
+@_on_stream
+def glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out=None, dtype="bf16", workspace=None, _s=0):
+    """moeq_glu_i8: silu(G) * U with G, U the products of xq with the int8
+    weights [N][K] of both projections, as matmul_i8."""
+    return _i8("glu_i8", 2, xq, xs, [(w_gate, s_gate), (w_up, s_up)], out, dtype, workspace, _s)
+
+
+def _glu_common(x, w_gate, w_up, gu, what):
+    _need(x.dim() == 2 and w_gate.dim() == 2, f"{what}: operands are not 2-D")
+    T, H = x.shape
+    N = w_gate.shape[0]
+    dev, dt = x.get_device(), x.dtype
+    act = _act(x, f"{what}: x")
+    if gu is not None:
+        _need(gu.is_cuda and gu.get_device() == dev and gu.dtype is dt and tuple(gu.shape) == (2, T, N)
+              and gu.is_contiguous(), f"{what}: gu is not a contiguous {dt} {(2, T, N)} on cuda:{dev}")
+    head = (T, H, N, act, x.data_ptr(), _ld(x, (T, H), dt, dev, f"{what}: x"), w_gate.data_ptr(), w_up.data_ptr(),
+            _ld(w_gate, (N, H), dt, dev, f"{what}: w_gate"), _ld(w_up, (N, H), dt, dev, f"{what}: w_up"),
+            gu.data_ptr() if gu is not None else 0)
+    return T, H, N, dev, dt, head
+
+
+@_on_stream
+def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, _s=0):
+    """moeq_glu: h = silu(x w_gate^T) * (x w_up^T), [T][N], for x [T][H] and
+    weights [N][H] (float32 or bfloat16, unit column stride).  With ``save``
+    (or a ``gu`` buffer [2][T][N]) returns (h, gu) with both projections kept
+    for glu_backward."""
+    import torch
+    if save and gu is None and x.dim() == 2 and w_gate.dim() == 2:
+        gu = torch.empty((2, x.shape[0], w_gate.shape[0]), dtype=x.dtype, device=x.device)
+    T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, "glu")
+    if out is None:
+        out = torch.empty((T, N), dtype=dt, device=x.device)
+    ldh = _ld(out, (T, N), dt, dev, "glu: out")
+    rest = (out.data_ptr(), ldh, 0, 0, 0, 0, 0, 0, 0, 0)
+    _call("moeq_glu", "moeq_glu_workspace", 0, lambda p, n: GLU_ARGS.pack(*head, *rest, p, n), workspace, dev, _s)
+    return out if gu is None else (out, gu)
+
+
+@_on_stream
+def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None, need_dx=True, need_dw=True,
+                 workspace=None, _s=0):
+    """moeq_glu_backward: (dx [T][H], dw_gate [N][H], dw_up [N][H]) for the
+    gradient dh [T][N] of glu's result; ``gu`` as kept by glu, or None to
+    compute the projections again.  Gradients left out (``need_dx``,
+    ``need_dw``) come back as None."""
+    import torch
+    T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, "glu_backward")
+    _need((dx is None or need_dx) and ((dw_gate is None and dw_up is None) or need_dw),
+          "glu_backward: a buffer for a gradient that is left out")
+    _need(need_dx or need_dw, "glu_backward: no gradient asked for")
+    if need_dx and dx is None:
+        dx = torch.empty((T, H), dtype=dt, device=x.device)
+    if need_dw:
+        if dw_gate is None:
+            dw_gate = torch.empty((N, H), dtype=dt, device=x.device)
+        if dw_up is None:
+            dw_up = torch.empty((N, H), dtype=dt, device=x.device)
+    rest = [0, 0, dh.data_ptr(), _ld(dh, (T, N), dt, dev, "glu_backward: dh")]
+    rest += [dx.data_ptr(), _ld(dx, (T, H), dt, dev, "glu_backward: dx")] if need_dx else [0, 0]
+    if need_dw:
+        rest += [dw_gate.data_ptr(), dw_up.data_ptr(), _ld(dw_gate, (N, H), dt, dev, "glu_backward: dw_gate"),
+                 _ld(dw_up, (N, H), dt, dev, "glu_backward: dw_up")]
+    else:
+        rest += [0, 0, 0, 0]
+    _call("moeq_glu_backward", "moeq_glu_workspace", 1, lambda p, n: GLU_ARGS.pack(*head, *rest, p, n), workspace,
+          dev, _s)
+    return dx, dw_gate, dw_up
+
+
+def dense_status(clear=False) -> int:
+    """moeq_dense_status: the current device's status word of the dense operators."""
+    return int(_lib.moeq_dense_status(1 if clear else 0))
 
 
 class Layer:

@@ -335,6 +335,137 @@ MOEQ_API moeq_status moeq_vq_encode(const float *w, int32_t n_rows, int32_t n_co
                                     const float *col_weight, const uint16_t *book13, const uint16_t *book8,
                                     uint8_t *idx13_out, uint8_t *idx8_out, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense operators: the gated block of a layer that is not routed (the model's
+ * first layer is dense) in f32 and bf16 with its backward pass, and the same
+ * block and a plain projection on 8-bit integers.  They need no layer handle:
+ * every array is the caller's, on the current device, and the calls allocate
+ * nothing.  Matrices are row-major with unit column stride and a row stride
+ * ("ld", in elements, at least the row length), so slices of wider buffers
+ * can be passed.  No alignment is asked for beyond an element's own; base
+ * addresses and row strides that are multiples of 16 bytes avoid a padded
+ * copy of the operand in the workspace.  An output may not overlap an input
+ * or another output (column windows of one buffer with one row stride do not
+ * overlap).  Columns between a row's end and the next row, and everything
+ * behind the last row, are left as they were.
+ *
+ * All calls are asynchronous on `stream` and keep no state between calls but
+ * the device's status word (moeq_dense_status); calls on several streams may
+ * overlap as long as their outputs and workspaces are their own, and every
+ * call may be captured into a CUDA graph (which then owns the workspace for
+ * as long as it may be replayed).
+ * ------------------------------------------------------------------------- */
+
+/* Rows to 8-bit integers, one scale each: for row r with a = max_c |x[r][c]|
+ *     scale[r] = a / 127                       (f32, round to nearest even)
+ *     q[r][c]  = 127 x[r][c] / a               rounded to the nearest integer,
+ *                                              halves to the even one
+ * so that x ~ q * scale, |q| <= 127.  The integer is that of the exact
+ * quotient (no rounding before the rounding).  A row of zeros gets q = 0,
+ * scale = 0; a row that holds a NaN or an infinity gets q = 0, scale = NaN,
+ * which makes its products NaN.  Serves activations (a row is a token) and
+ * weights (a row is an output channel).
+ *   x      device, dtype (moeq_dtype), [n_rows][n_cols], row stride ldx
+ *   q      device int8 [n_rows][n_cols], row stride ldq; overwritten
+ *   scale  device f32 [n_rows]; overwritten
+ * n_rows == 0 is a no-op.  Errors: INVALID_ARGUMENT (NULL, sizes, strides,
+ * unknown dtype, misaligned elements, overlap), CUDA. */
+MOEQ_API moeq_status moeq_quant_i8(const void *x, int32_t dtype, int32_t n_rows, int32_t n_cols, int64_t ldx,
+                                   int8_t *q, int64_t ldq, float *scale, void *stream);
+
+/* Arguments of moeq_matmul_i8 and moeq_glu_i8. */
+typedef struct {
+    int32_t n_tokens;         /* T >= 0 (0: no-op)                              */
+    int32_t n_in;             /* K, 1..131071 (a sum of K products fits int32)  */
+    int32_t n_out;            /* N >= 1                                         */
+    int32_t out_dtype;        /* moeq_dtype of out                              */
+    const int8_t *x;          /* device [T][K], row stride ldx                  */
+    int64_t ldx;
+    const float *x_scale;     /* device f32 [T]: one scale per token            */
+    const int8_t *w[2];       /* device [N][K], row strides ldw; matmul: w[0]   */
+    int64_t ldw[2];           /*   only; glu: gate, up                          */
+    const float *w_scale[2];  /* device f32 [N] each: one scale per channel     */
+    void *out;                /* device [T][N], row stride ldo; overwritten     */
+    int64_t ldo;
+    void *workspace;          /* device, 256-byte aligned, or NULL if 0 bytes   */
+    int64_t workspace_bytes;
+} moeq_i8_args;
+
+/* out[t][n] = (sum_k x[t][k] w[n][k]) x_scale[t] w_scale[n]: the sum is exact
+ * (32-bit integers), then two f32 products in that order and one rounding to
+ * out_dtype.  Entries of w[1], ldw[1] and w_scale[1] must be NULL / 0.
+ * Errors: INVALID_ARGUMENT (NULL, sizes, strides, unknown dtype, misaligned
+ * elements, overlap, a workspace that is too small or misaligned), CUDA. */
+MOEQ_API moeq_status moeq_matmul_i8(const moeq_i8_args *a, void *stream);
+
+/* The gated block on 8-bit integers: with G and U the products of x with w[0]
+ * and w[1] as in moeq_matmul_i8 (f32),
+ *     out[t][n] = silu(G[t][n]) U[t][n],   silu(z) = z / (1 + e^-z),
+ * in f32, rounded once to out_dtype.  Errors: as moeq_matmul_i8. */
+MOEQ_API moeq_status moeq_glu_i8(const moeq_i8_args *a, void *stream);
+
+/* Bytes of workspace that a call with these arguments needs (workspace and
+ * workspace_bytes are not looked at); 0 for most, -1 for invalid arguments.
+ * n_w: 1 for moeq_matmul_i8, 2 for moeq_glu_i8. */
+MOEQ_API int64_t moeq_i8_workspace(const moeq_i8_args *a, int32_t n_w);
+
+/* Arguments of moeq_glu and moeq_glu_backward; each reads the fields that its
+ * description names. */
+typedef struct {
+    int32_t n_tokens;         /* T >= 0                                         */
+    int32_t hidden;           /* H >= 1                                         */
+    int32_t inter;            /* I >= 1                                         */
+    int32_t dtype;            /* moeq_dtype of every array                      */
+    const void *x;            /* device [T][H], row stride ldx                  */
+    int64_t ldx;
+    const void *w[2];         /* device [I][H], row strides ldw: gate, up       */
+    int64_t ldw[2];
+    void *gu;                 /* device [2][T][I] without gaps, or NULL: the    */
+                              /* projections (gate plane, up plane)             */
+    void *h;                  /* device [T][I], row stride ldh                  */
+    int64_t ldh;
+    const void *dh;           /* device [T][I], row stride lddh                 */
+    int64_t lddh;
+    void *dx;                 /* device [T][H], row stride lddx, or NULL        */
+    int64_t lddx;
+    void *dw[2];              /* device [I][H], row strides lddw, or both NULL  */
+    int64_t lddw[2];
+    void *workspace;          /* device, 256-byte aligned, or NULL if 0 bytes   */
+    int64_t workspace_bytes;
+} moeq_glu_args;
+
+/* h[t] = silu(W_gate x[t]) * (W_up x[t]): both projections (f32 sums), the
+ * activation and the product in one pass, rounded once to dtype.  With gu,
+ * the two projections are also written, rounded to dtype, for a backward
+ * pass.  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.  Errors:
+ * INVALID_ARGUMENT (NULL, sizes, strides, unknown dtype, misaligned elements,
+ * overlap, a workspace that is too small or misaligned), CUDA. */
+MOEQ_API moeq_status moeq_glu(const moeq_glu_args *a, void *stream);
+
+/* The gradients of moeq_glu for the gradient dh of its result.  With g, u the
+ * projections and s = 1 / (1 + e^-g),
+ *     dg = dh u s (1 + g (1 - s)),   du = dh g s
+ *     dx = dg W_gate + du W_up,   dW_gate = dg^T x,   dW_up = du^T x
+ * g and u are read from gu where it is given (as moeq_glu wrote it), else
+ * computed again from x and w.  dg and du are rounded to dtype (they are the
+ * operands of the products that follow); sums are f32, rounded once.  Outputs
+ * are overwritten; dx NULL or both dw NULL leaves that gradient out (not
+ * both).  Reads x, w, gu, dh; h is not read.  n_tokens == 0 sets dw to zero.
+ * Errors: as moeq_glu. */
+MOEQ_API moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream);
+
+/* Bytes of workspace that a call with these arguments needs (workspace and
+ * workspace_bytes are not looked at), -1 for invalid arguments.  backward: 0
+ * for moeq_glu, 1 for moeq_glu_backward. */
+MOEQ_API int64_t moeq_glu_workspace(const moeq_glu_args *a, int32_t backward);
+
+/* The current device's status word of the dense operators, read after
+ * synchronizing the device: MOEQ_OK, or MOEQ_ERR_TIMEOUT when a kernel's
+ * bounded wait on another part of the same kernel gave up (never expected in
+ * normal operation; that call's output is undefined, the device stays
+ * usable).  clear != 0 resets it.  Errors: CUDA. */
+MOEQ_API moeq_status moeq_dense_status(int32_t clear);
+
 /* moeq_forward that also records five caller-created CUDA events (passed
  * as cudaEvent_t cast to void*) on `stream` at its phase boundaries:
  * events[0] before the first launch, [1] after route/bucket, [2] after the
