@@ -61,7 +61,15 @@ __device__ __forceinline__ void st_elem(float *p, float v) { *p = v; }
 __device__ __forceinline__ void st_elem(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // ---- launchers ----
+// f32, any strides and alignment (dense_simt.cu)
 cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
+// bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
+cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
+// dst (16-byte aligned base and row stride) = src, rows x cols of es-byte elements
+cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_ld, long long rows, long long cols,
+                        int es, cudaStream_t s);
+// Address of the current device's status word (dense_tc.cu).
+cudaError_t status_word(uint32_t **p);
 // dgu[0/1] (row stride ld) = the gradients of the kept projections gu [2][M][N]
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,
                              long long M, long long N, int dtype, cudaStream_t s);

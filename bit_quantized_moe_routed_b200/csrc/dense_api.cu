@@ -15,6 +15,7 @@ namespace dense {
 namespace {
 
 constexpr long long kMaxDim = 1LL << 21;      // hidden, inter, n_in, n_out
+constexpr int kMaxTokens = 1 << 30;
 constexpr long long kMaxLd = 1LL << 36;
 constexpr int kMaxI8K = 131071;               // 2^14 K < 2^31
 
@@ -59,15 +60,42 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 moeq_status done(cudaError_t e) { return e == cudaSuccess ? MOEQ_OK : MOEQ_ERR_CUDA; }
 
-// Sizes of the workspace's parts, in the order they lie in it.
+// An operand of the tensor-core kernels that does not start its rows on
+// 16-byte addresses is copied into the workspace with padded rows first.
+struct Packed {
+    size_t bytes = 0;          // 0: used where it lies
+    long long ld = 0;
+    Packed() {}
+    Packed(const void *p, long long rows, long long cols, long long ld_, int es) {
+        if (!((uintptr_t)p & 15u) && (rows <= 1 || !((ld_ * es) & 15))) return;
+        ld = (cols * es + 127) / 128 * 128 / es;
+        bytes = round256((size_t)rows * ld * es);
+    }
+};
+// The workspace's parts, in the order they lie in it.
 struct Plan {
+    Packed x, w[2];
     size_t dgu = 0;            // gradients of the projections, [2][T][dgu_ld]
     long long dgu_ld = 0;
-    size_t total() const { return dgu; }
+    size_t total() const { return x.bytes + w[0].bytes + w[1].bytes + dgu; }
 };
+// Where an operand of rows x cols lies for the kernels: itself, or (after
+// this copy) the next part of the workspace.
+cudaError_t place(const Packed &k, const void *&p, long long &ld, long long rows, long long cols, int es, char *&ws,
+                  cudaStream_t s) {
+    if (!k.bytes) return cudaSuccess;
+    const cudaError_t e = launch_pack(p, ld, ws, k.ld, rows, cols, es, s);
+    p = ws;
+    ld = k.ld;
+    ws += k.bytes;
+    return e;
+}
+cudaError_t launch_product(const Product &p, cudaStream_t s) {
+    return p.in_dtype == MOEQ_ACT_F32 ? launch_product_simt(p, s) : launch_product_tc(p, s);
+}
 
 bool i8_args_ok(const moeq_i8_args *a, int nw) {
-    if (!a || (nw != 1 && nw != 2) || a->n_tokens < 0 || a->n_in < 1 || a->n_in > kMaxI8K || a->n_out < 1 ||
+    if (!a || (nw != 1 && nw != 2) || a->n_tokens < 0 || a->n_tokens > kMaxTokens || a->n_in < 1 || a->n_in > kMaxI8K || a->n_out < 1 ||
         a->n_out > kMaxDim || !known_dtype(a->out_dtype))
         return false;
     const bool any = a->n_tokens > 0;   // the arrays of no tokens may be NULL
@@ -80,10 +108,16 @@ bool i8_args_ok(const moeq_i8_args *a, int nw) {
     if (nw == 1 && (a->w[1] || a->ldw[1] || a->w_scale[1])) return false;
     return true;
 }
-Plan plan_i8(const moeq_i8_args *, int) { return Plan(); }
+Plan plan_i8(const moeq_i8_args *a, int nw) {
+    Plan p;
+    if (a->n_tokens == 0) return p;
+    p.x = Packed(a->x, a->n_tokens, a->n_in, a->ldx, 1);
+    for (int i = 0; i < nw; ++i) p.w[i] = Packed(a->w[i], a->n_out, a->n_in, a->ldw[i], 1);
+    return p;
+}
 
 bool glu_args_ok(const moeq_glu_args *a, bool backward) {
-    if (!a || a->n_tokens < 0 || a->hidden < 1 || a->hidden > kMaxDim || a->inter < 1 || a->inter > kMaxDim ||
+    if (!a || a->n_tokens < 0 || a->n_tokens > kMaxTokens || a->hidden < 1 || a->hidden > kMaxDim || a->inter < 1 || a->inter > kMaxDim ||
         !known_dtype(a->dtype))
         return false;
     const int es = elem_size(a->dtype);
@@ -103,7 +137,13 @@ bool glu_args_ok(const moeq_glu_args *a, bool backward) {
 }
 Plan plan_glu(const moeq_glu_args *a, bool backward) {
     Plan p;
-    if (!backward || a->n_tokens == 0) return p;
+    if (a->n_tokens == 0) return p;
+    if (a->dtype == MOEQ_ACT_BF16) {
+        if (!backward || !a->gu || a->dw[0]) p.x = Packed(a->x, a->n_tokens, a->hidden, a->ldx, 2);
+        if (!backward || !a->gu || a->dx)
+            for (int i = 0; i < 2; ++i) p.w[i] = Packed(a->w[i], a->inter, a->hidden, a->ldw[i], 2);
+    }
+    if (!backward) return p;
     p.dgu_ld = (a->inter + 63) / 64 * 64;
     p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * elem_size(a->dtype));
     return p;
@@ -142,7 +182,10 @@ moeq_status run_i8(const moeq_i8_args *a, int nw, cudaStream_t s) {
     p.in_dtype = kI8;
     p.out_dtype = a->out_dtype;
     p.epi = nw == 2 ? EPI_GLU : EPI_STORE;
-    return done(launch_product_simt(p, s));
+    char *ws = (char *)a->workspace;
+    cudaError_t e = place(plan.x, p.a[0], p.ald, T, K, 1, ws, s);
+    for (int i = 0; i < nw && e == cudaSuccess; ++i) e = place(plan.w[i], p.b[i], p.bld[i], N, K, 1, ws, s);
+    return done(e == cudaSuccess ? launch_product(p, s) : e);
 }
 
 }  // namespace
@@ -206,7 +249,11 @@ extern "C" moeq_status moeq_glu(const moeq_glu_args *a, void *stream) {
     p.old[0] = a->ldh;
     p.in_dtype = p.out_dtype = a->dtype;
     p.epi = EPI_GLU;
-    return done(launch_product_simt(p, (cudaStream_t)stream));
+    const cudaStream_t s = (cudaStream_t)stream;
+    char *ws = (char *)a->workspace;
+    cudaError_t e = place(plan.x, p.a[0], p.ald, T, H, es, ws, s);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = place(plan.w[i], p.b[i], p.bld[i], I, H, es, ws, s);
+    return done(e == cudaSuccess ? launch_product(p, s) : e);
 }
 
 extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
@@ -230,8 +277,13 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         }
         return MOEQ_OK;
     }
-    char *dg = (char *)a->workspace, *du = dg + (size_t)T * plan.dgu_ld * es;
-    cudaError_t e;
+    char *ws = (char *)a->workspace;
+    const void *x = a->x, *w[2] = {a->w[0], a->w[1]};
+    long long ldx = a->ldx, ldw[2] = {a->ldw[0], a->ldw[1]};
+    cudaError_t e = place(plan.x, x, ldx, T, H, es, ws, s);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = place(plan.w[i], w[i], ldw[i], I, H, es, ws, s);
+    if (e != cudaSuccess) return MOEQ_ERR_CUDA;
+    char *dg = ws, *du = dg + (size_t)T * plan.dgu_ld * es;
     if (a->gu) {
         e = launch_glu_dgate(a->dh, a->lddh, a->gu, dg, du, plan.dgu_ld, T, I, a->dtype, s);
     } else {
@@ -239,11 +291,11 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         p.M = T;
         p.N = I;
         p.K = H;
-        p.a[0] = a->x;
-        p.ald = a->ldx;
+        p.a[0] = x;
+        p.ald = ldx;
         for (int i = 0; i < 2; ++i) {
-            p.b[i] = a->w[i];
-            p.bld[i] = a->ldw[i];
+            p.b[i] = w[i];
+            p.bld[i] = ldw[i];
         }
         p.keep[0] = dg;
         p.keep[1] = du;
@@ -252,7 +304,7 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         p.dhld = a->lddh;
         p.in_dtype = p.out_dtype = a->dtype;
         p.epi = EPI_GLU_BWD;
-        e = launch_product_simt(p, s);
+        e = launch_product(p, s);
     }
     if (e == cudaSuccess && a->dx) {
         Product p;   // dx = dg W_gate + du W_up: two segments along the reduction
@@ -265,13 +317,13 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         p.ald = plan.dgu_ld;
         p.b_t = true;
         for (int i = 0; i < 2; ++i) {
-            p.b[i] = a->w[i];
-            p.bld[i] = a->ldw[i];
+            p.b[i] = w[i];
+            p.bld[i] = ldw[i];
         }
         p.out[0] = a->dx;
         p.old[0] = a->lddx;
         p.in_dtype = p.out_dtype = a->dtype;
-        e = launch_product_simt(p, s);
+        e = launch_product(p, s);
     }
     if (e == cudaSuccess && a->dw[0]) {
         Product p;   // dW_i = d_i^T x: two products of one B
@@ -283,29 +335,22 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         p.a[1] = du;
         p.ald = plan.dgu_ld;
         p.a_t = p.b_t = true;
-        p.b[0] = a->x;
-        p.bld[0] = a->ldx;
+        p.b[0] = x;
+        p.bld[0] = ldx;
         for (int i = 0; i < 2; ++i) {
             p.out[i] = a->dw[i];
             p.old[i] = a->lddw[i];
         }
         p.in_dtype = p.out_dtype = a->dtype;
-        e = launch_product_simt(p, s);
+        e = launch_product(p, s);
     }
     return done(e);
 }
 
-namespace {
-__device__ uint32_t g_dense_status;
-}
-
 extern "C" moeq_status moeq_dense_status(int32_t clear) {
-    if (cudaDeviceSynchronize() != cudaSuccess) return MOEQ_ERR_CUDA;
-    uint32_t w = 0;
-    if (cudaMemcpyFromSymbol(&w, g_dense_status, sizeof(w)) != cudaSuccess) return MOEQ_ERR_CUDA;
-    if (clear && w) {
-        const uint32_t zero = 0;
-        if (cudaMemcpyToSymbol(g_dense_status, &zero, sizeof(zero)) != cudaSuccess) return MOEQ_ERR_CUDA;
-    }
+    uint32_t *at = nullptr, w = 0;
+    if (status_word(&at) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return MOEQ_ERR_CUDA;
+    if (cudaMemcpy(&w, at, sizeof(w), cudaMemcpyDeviceToHost) != cudaSuccess) return MOEQ_ERR_CUDA;
+    if (clear && w && cudaMemset(at, 0, sizeof(w)) != cudaSuccess) return MOEQ_ERR_CUDA;
     return w ? MOEQ_ERR_TIMEOUT : MOEQ_OK;
 }

@@ -1,0 +1,472 @@
+// dense_tc.cu -- products of the dense operators on the tensor cores, many
+// rows: out[M][N] tiles of 256 x BN by pairs of SMs (tcgen05 cta_group::2).
+//
+// Mathematics: D = A B^T with A [M][K], B [N][K], each stored with K
+// contiguous or (bf16) transposed with M / N contiguous; sums in f32 (bf16) or
+// exact in s32 (int8).  The gated block multiplies A with two matrices at
+// once: a pair's B tile is BN/2 rows of gate (loaded by the first SM) and the
+// same BN/2 rows of up (by the second), so one accumulator row holds the gate
+// and up sums of the same outputs and the epilogue forms silu(g) u, or the
+// gradients dg, du, without another pass.  dx = dg Wg + du Wu runs its
+// reduction over two segments into one accumulator; dWg and dWu are two
+// batches over one B.
+//
+// Bound: the tensor cores.  Each K block of 128 bytes (64 bf16, 128 s8) is 16
+// KB of A and BN/2 x 128 bytes of B per SM, loaded by TMA (128-byte swizzle)
+// into a ring of stages; a pair reads every byte of its tile once per K block,
+// so 256 x 256 tiles need 256 flop per byte from L2.  Roles per SM: warp 0
+// loads, warp 1 of the first SM issues the MMAs for both, warps 4..11 run the
+// epilogue of one accumulator while the MMAs fill the other (two of BN columns
+// in tensor memory).  Persistent pairs walk the tiles in groups of 8 tile rows
+// so that the tiles in flight share operands in L2.
+//
+// Every wait is bounded: a role that gives up raises the CTA's abort flag, the
+// kernel drains its copies and MMAs, frees its tensor memory and raises the
+// status word.
+#include <atomic>
+#include <mutex>
+
+#include "dense_tc.cuh"
+
+namespace moeq {
+namespace dense {
+namespace {
+
+using namespace umma;
+
+constexpr int kTileM = 128;                 // rows of A per SM (a pair: 256)
+constexpr int kABytes = kTileM * kRowBytes; // 16 KB
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kStageOut = kEpiWarps * 4096;
+constexpr int kGroupM = 8;
+
+struct TcArgs {
+    CUtensorMap a[2], b[2];
+    long long M, N;
+    int kblocks;         // K blocks of one segment
+    int nseg, nbatch;
+    int mt, nt;          // tiles of one batch
+    const float *a_scale, *b_scale[2];
+    void *out[2];
+    long long old[2];
+    void *keep[2];
+    long long kld;
+    const void *dh;
+    long long dhld;
+    bool vec_out, vec_keep, vec_dh;
+    uint32_t *status;
+};
+
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <bool I8>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if (I8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// Arrive on `bar` of both SMs once every MMA issued so far has completed.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int BN>
+struct Ring {
+    static constexpr int kBBytes = BN / 2 * kRowBytes;
+    static constexpr int kStage = kABytes + kBBytes;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + kStageOut + 1024;
+};
+
+// tile index -> batch, tile row, tile column: groups of kGroupM tile rows, row fastest
+struct TileAt {
+    int z, m, n;
+    __device__ __forceinline__ TileAt(int t, int mt, int nt) {
+        z = t / (mt * nt);
+        t -= z * mt * nt;
+        const int per = kGroupM * nt, g = t / per, first = g * kGroupM;
+        const int rows = min(kGroupM, mt - first);
+        t -= g * per;
+        m = first + t % rows;
+        n = t / rows;
+    }
+};
+
+template <bool I8, bool A_MN, bool B_MN, int EPI, int BN, typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product_tc_kernel(const __grid_constant__
+                                                                                          TcArgs p) {
+    typedef Ring<BN> R;
+    constexpr int S = R::kStages;
+    constexpr int kKE = I8 ? 128 : 64;                       // elements of a K block
+    constexpr int kOutN = EPI == EPI_STORE ? BN : BN / 2;    // columns of out per tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *stage_out = smem + S * R::kStage;
+    __shared__ alignas(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&done, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(2 * BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = p.mt * p.nt * p.nbatch;
+    const int kb_total = p.kblocks * p.nseg;
+
+    if (warp == 0 && lane == 0) {
+        // ---- loads: this SM's 128 rows of A and its half of B, into the pair's barrier
+        int c = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+            const TileAt at(t, p.mt, p.nt);
+            const int m0 = at.m * 2 * kTileM + (int)rank * kTileM;
+            const int n0 = EPI == EPI_STORE ? at.n * BN + (int)rank * (BN / 2) : at.n * kOutN;
+            for (int kb = 0; kb < kb_total; ++kb, ++c) {
+                const int s = c % S, seg = p.nseg > 1 && kb >= p.kblocks, k0 = (seg ? kb - p.kblocks : kb) * kKE;
+                if (c >= S && !wait_cluster(&empty[s], (uint32_t)((c / S - 1) & 1), &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
+                const uint32_t bar = in_cta(&full[s], 0);
+                uint8_t *sa = smem + s * R::kStage, *sb = sa + kABytes;
+                const CUtensorMap *ma = &p.a[p.nseg > 1 ? seg : at.z];
+                const CUtensorMap *mb = &p.b[EPI == EPI_STORE ? seg : (int)rank];
+                if (A_MN) {
+#pragma unroll
+                    for (int j = 0; j < kTileM / 64; ++j) tma_load_pair(sa + j * 8192, ma, m0 + 64 * j, k0, bar);
+                } else {
+                    tma_load_pair(sa, ma, k0, m0, bar);
+                }
+                if (B_MN) {
+#pragma unroll
+                    for (int j = 0; j < BN / 128; ++j) tma_load_pair(sb + j * 8192, mb, n0 + 64 * j, k0, bar);
+                } else {
+                    tma_load_pair(sb, mb, k0, n0, bar);
+                }
+            }
+        }
+        // the ring's last stages: consumed before this SM's shared memory goes away
+        for (int i = c > S ? c - S : 0; i < c; ++i) {
+            const long long t0 = clock64();
+            while (!test_wait_cluster(&empty[i % S], (uint32_t)((i / S) & 1)) &&
+                   clock64() - t0 < (ok ? kWaitCycles : kDrainCycles)) {
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- MMAs of the pair
+        constexpr uint32_t id = idesc_dense<I8>(2 * kTileM, BN, A_MN, B_MN);
+        int c = 0, q = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs, ++q) {
+            const int b = q & 1;
+            if (q >= 2 && !wait_cluster(&acc_empty[b], (uint32_t)(((q >> 1) - 1) & 1), &abort_flag)) break;
+            tc_fence_after();
+            for (int kb = 0; kb < kb_total; ++kb, ++c) {
+                const int s = c % S;
+                if (!wait_cluster(&full[s], (uint32_t)((c / S) & 1), &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint8_t *sa = smem + s * R::kStage, *sb = sa + kABytes;
+                const uint64_t da = A_MN ? desc_mn_sw128(sa, 8192) : desc_sw128(sa);
+                const uint64_t db = B_MN ? desc_mn_sw128(sb, 8192) : desc_sw128(sb);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // 32 bytes of K each: 16 bf16 or 32 s8
+                    mma_pair<I8>(tmem + b * BN, da + k * (A_MN ? 2048 >> 4 : 32 >> 4),
+                                 db + k * (B_MN ? 2048 >> 4 : 32 >> 4), id, (kb | k) != 0);
+                commit_pair(&empty[s]);
+            }
+            if (ok) commit_pair(&acc_full[b]);
+        }
+        if (abort_flag) {   // MMAs in flight end before the tensor memory goes away
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done))
+                         : "memory");
+            mbar_wait_bounded(&done, 0, kDrainCycles);
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue: warp w reads lanes 32 (w % 4).., columns by halves
+        const int e = warp - 4, quad = e & 3, half = e >> 2;
+        uint8_t *stage = stage_out + e * 4096;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+        int q = 0;
+        for (int t = pair; t < tiles; t += pairs, ++q) {
+            const TileAt at(t, p.mt, p.nt);
+            const int b = q & 1;
+            if (!wait_cluster(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag)) break;
+            tc_fence_after();
+            const long long m0 = (long long)at.m * 2 * kTileM + rank * kTileM + quad * 32, n0 = (long long)at.n * kOutN;
+            const int rows = (int)min(32LL, p.M - m0);
+            const float sx = I8 && lane < rows ? __ldg(p.a_scale + m0 + lane) : 0.f;
+            O *out = static_cast<O *>(p.out[at.z]);
+#pragma unroll 1
+            for (int c0 = half * (kOutN / 2); c0 < (half + 1) * (kOutN / 2); c0 += 32) {
+                const long long n = n0 + c0;
+                const int cols = (int)max(0LL, min(32LL, p.N - n));
+                uint32_t r0[32], r1[32];
+                tmem_ld32(lane_base + b * BN + c0, r0);
+                if (EPI != EPI_STORE) tmem_ld32(lane_base + b * BN + BN / 2 + c0, r1);
+                tmem_ld_wait();
+                if (rows <= 0 || cols <= 0) continue;
+                float g[32], u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (I8) {
+                        const bool in = i < cols;
+                        g[i] = (float)(int)r0[i] * sx * (in ? __ldg(p.b_scale[0] + n + i) : 0.f);
+                        if (EPI != EPI_STORE) u[i] = (float)(int)r1[i] * sx * (in ? __ldg(p.b_scale[1] + n + i) : 0.f);
+                    } else {
+                        g[i] = __uint_as_float(r0[i]);
+                        if (EPI != EPI_STORE) u[i] = __uint_as_float(r1[i]);
+                    }
+                }
+                if (EPI == EPI_STORE) {
+                    store_32x32<O>(stage, g, out + m0 * p.old[at.z] + n, p.old[at.z], rows, cols, p.vec_out);
+                } else if (EPI == EPI_GLU) {
+                    if (!I8 && p.keep[0]) {
+                        store_32x32<O>(stage, g, static_cast<O *>(p.keep[0]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
+                        store_32x32<O>(stage, u, static_cast<O *>(p.keep[1]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) g[i] = silu_f32(g[i]) * u[i];
+                    store_32x32<O>(stage, g, out + m0 * p.old[0] + n, p.old[0], rows, cols, p.vec_out);
+                } else {
+                    const O *dh = static_cast<const O *>(p.dh) + (m0 + lane) * p.dhld + n;
+                    if (p.vec_dh && cols == 32 && lane < rows && sizeof(O) == 2) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(dh) + j);
+                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float d = bf16_bits_to_f32(i & 1 ? ww[i >> 1] >> 16 : ww[i >> 1] & 0xFFFFu);
+                                glu_grad(g[8 * j + i], u[8 * j + i], d, g[8 * j + i], u[8 * j + i]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float d = lane < rows && i < cols ? ld_elem(dh + i) : 0.f;
+                            glu_grad(g[i], u[i], d, g[i], u[i]);
+                        }
+                    }
+                    store_32x32<O>(stage, g, static_cast<O *>(p.keep[0]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
+                    store_32x32<O>(stage, u, static_cast<O *>(p.keep[1]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(in_cta(&acc_empty[b], 0));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // ends: every wait above is bounded
+    tc_fence_after();
+    if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, FLAG_TIMEOUT);
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+}
+
+template <bool I8, bool A_MN, bool B_MN, int EPI, int BN, typename O>
+cudaError_t launch_t(const Product &p, cudaStream_t s) {
+    constexpr int kKE = I8 ? 128 : 64, es = I8 ? 1 : 2;
+    constexpr int kOutN = EPI == EPI_STORE ? BN : BN / 2;
+    typedef Ring<BN> R;
+    TcArgs a{};
+    cudaError_t e = cudaSuccess;
+    const int na = p.nseg > 1 || p.nbatch > 1 ? 2 : 1, nb = EPI == EPI_STORE ? p.nseg : 2;
+    for (int i = 0; i < na && e == cudaSuccess; ++i)
+        e = A_MN ? make_map(&a.a[i], p.a[i], p.K, p.M, p.ald, es, 64)
+                 : make_map(&a.a[i], p.a[i], p.M, p.K, p.ald, es, kTileM);
+    for (int i = 0; i < nb && e == cudaSuccess; ++i)
+        e = B_MN ? make_map(&a.b[i], p.b[i], p.K, p.N, p.bld[i], es, 64)
+                 : make_map(&a.b[i], p.b[i], p.N, p.K, p.bld[i], es, BN / 2);
+    if (e != cudaSuccess) return e;
+    a.M = p.M;
+    a.N = p.N;
+    a.kblocks = (int)((p.K + kKE - 1) / kKE);
+    a.nseg = p.nseg;
+    a.nbatch = p.nbatch;
+    a.mt = (int)((p.M + 2 * kTileM - 1) / (2 * kTileM));
+    a.nt = (int)((p.N + kOutN - 1) / kOutN);
+    const int so = (int)sizeof(O);
+    a.vec_out = true;
+    for (int i = 0; i < 2; ++i) {
+        a.b_scale[i] = p.b_scale[i];
+        a.out[i] = p.out[i];
+        a.old[i] = p.old[i];
+        a.keep[i] = p.keep[i];
+        if (p.out[i] && (((uintptr_t)p.out[i] & 15u) || (p.old[i] * so & 15))) a.vec_out = false;
+    }
+    a.a_scale = p.a_scale;
+    a.kld = p.kld;
+    a.dh = p.dh;
+    a.dhld = p.dhld;
+    a.vec_keep = !((uintptr_t)p.keep[0] & 15u) && !((uintptr_t)p.keep[1] & 15u) && !(p.kld * so & 15);
+    a.vec_dh = !((uintptr_t)p.dh & 15u) && !(p.dhld * so & 15);
+    int sms = 0;
+    e = status_word(&a.status);
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const auto kernel = product_tc_kernel<I8, A_MN, B_MN, EPI, BN, O>;
+    {
+        static std::mutex mu;
+        static bool ready[64] = {};
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev >= 64 || !ready[dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::kSmem);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) ready[dev] = true;
+        }
+    }
+    const long long tiles = (long long)a.mt * a.nt * a.nbatch;
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
+    const int pairs = (int)std::min<long long>(tiles, sms / 2);
+    kernel<<<2 * pairs, kThreads, R::kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
+// Tile width: the one that leaves the pairs idle least.  A tile of 256
+// columns costs about BN + 24 (the fill of the ring and the epilogue's tail).
+template <bool I8, bool A_MN, bool B_MN, int EPI, typename O>
+cudaError_t launch_bn(const Product &p, cudaStream_t s) {
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    long long best = 0;
+    int bn = 256;
+    for (int w : {256, 128}) {
+        const long long cols = EPI == EPI_STORE ? w : w / 2;
+        const long long tiles = (p.M + 255) / 256 * ((p.N + cols - 1) / cols) * p.nbatch;
+        const long long cost = (tiles + sms / 2 - 1) / (sms / 2) * (w + 24);
+        if (w == 256 || cost < best) best = cost, bn = w;
+    }
+    return bn == 256 ? launch_t<I8, A_MN, B_MN, EPI, 256, O>(p, s) : launch_t<I8, A_MN, B_MN, EPI, 128, O>(p, s);
+}
+
+__device__ uint32_t g_status;
+
+}  // namespace
+
+cudaError_t status_word(uint32_t **p) {
+    static std::mutex mu;
+    static uint32_t *at[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && at[dev]) {
+        *p = at[dev];
+        return cudaSuccess;
+    }
+    void *q = nullptr;
+    e = cudaGetSymbolAddress(&q, g_status);
+    if (e == cudaSuccess) {
+        *p = static_cast<uint32_t *>(q);
+        if (dev < 64) at[dev] = *p;
+    }
+    return e;
+}
+
+cudaError_t sm_count(int *n) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*n, std::memory_order_relaxed);
+    return e;
+}
+
+cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long long cols, long long ld, int es,
+                     int box_rows) {
+    typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<EncodeFn> fn{nullptr};
+    EncodeFn f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+        f = reinterpret_cast<EncodeFn>(p);
+        fn.store(f, std::memory_order_release);
+    }
+    // a single row has no stride of its own
+    const long long pitch = rows > 1 ? ld * es : (cols * es + 15) / 16 * 16;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows};
+    const cuuint32_t es1[2] = {1, 1};
+    const CUresult r = f(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                         const_cast<void *>(base), dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_product_tc(const Product &p, cudaStream_t s) {
+    if (p.in_dtype == kI8) {
+        if (p.epi == EPI_GLU)
+            return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, false, EPI_GLU, float>(p, s)
+                                               : launch_bn<true, false, false, EPI_GLU, __nv_bfloat16>(p, s);
+        return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, false, EPI_STORE, float>(p, s)
+                                           : launch_bn<true, false, false, EPI_STORE, __nv_bfloat16>(p, s);
+    }
+    if (p.epi == EPI_GLU) return launch_bn<false, false, false, EPI_GLU, __nv_bfloat16>(p, s);
+    if (p.epi == EPI_GLU_BWD) return launch_bn<false, false, false, EPI_GLU_BWD, __nv_bfloat16>(p, s);
+    if (p.a_t) return launch_bn<false, true, true, EPI_STORE, __nv_bfloat16>(p, s);
+    return launch_bn<false, false, true, EPI_STORE, __nv_bfloat16>(p, s);
+}
+
+}  // namespace dense
+}  // namespace moeq

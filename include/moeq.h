@@ -375,9 +375,9 @@ MOEQ_API moeq_status moeq_quant_i8(const void *x, int32_t dtype, int32_t n_rows,
 
 /* Arguments of moeq_matmul_i8 and moeq_glu_i8. */
 typedef struct {
-    int32_t n_tokens;         /* T >= 0 (0: no-op)                              */
+    int32_t n_tokens;         /* T, 0 (a no-op) to 2^30                         */
     int32_t n_in;             /* K, 1..131071 (a sum of K products fits int32)  */
-    int32_t n_out;            /* N >= 1                                         */
+    int32_t n_out;            /* N, 1..2^21                                     */
     int32_t out_dtype;        /* moeq_dtype of out                              */
     const int8_t *x;          /* device [T][K], row stride ldx                  */
     int64_t ldx;
@@ -412,9 +412,9 @@ MOEQ_API int64_t moeq_i8_workspace(const moeq_i8_args *a, int32_t n_w);
 /* Arguments of moeq_glu and moeq_glu_backward; each reads the fields that its
  * description names. */
 typedef struct {
-    int32_t n_tokens;         /* T >= 0                                         */
-    int32_t hidden;           /* H >= 1                                         */
-    int32_t inter;            /* I >= 1                                         */
+    int32_t n_tokens;         /* T, 0..2^30                                     */
+    int32_t hidden;           /* H, 1..2^21                                     */
+    int32_t inter;            /* I, 1..2^21                                     */
     int32_t dtype;            /* moeq_dtype of every array                      */
     const void *x;            /* device [T][H], row stride ldx                  */
     int64_t ldx;
