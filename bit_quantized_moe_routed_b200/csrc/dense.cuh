@@ -45,10 +45,24 @@ struct Product {
 };
 constexpr int kI8 = 100;
 
-// silu and its derivative from the sigmoid s = 1 / (1 + e^-g)
-__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+// The sigmoid 1 / (1 + e^-g).  For bf16 results the exponential and the
+// divide are the hardware's approximations: off by at most 2 ulp and by
+// |g| 2^-23 (the rounding of g log2 e in the exponent), below 2^-16 wherever
+// e^-g stays in f32, against the 2^-9 of the rounding that follows; e^-g
+// beyond 2^126 (g < -87.3) gives 0 for a value below 2^-126.  The IEEE divide
+// and expf made the gated epilogue 10 us longer at 2048 x 4096 x 2048.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_f32(float g) {
+    return FAST ? __fdividef(1.0f, 1.0f + __expf(-g)) : 1.0f / (1.0f + expf(-g));
+}
+template <bool FAST>
+__device__ __forceinline__ float silu(float g) {
+    return FAST ? __fdividef(g, 1.0f + __expf(-g)) : silu_f32(g);
+}
+// dg and du for the gradient dh of silu(g) u
+template <bool FAST>
 __device__ __forceinline__ void glu_grad(float g, float u, float dh, float &dg, float &du) {
-    const float s = sigmoid_f32(g);
+    const float s = sigmoid_f32<FAST>(g);
     dg = dh * u * (s * (1.0f + g * (1.0f - s)));
     du = dh * (g * s);
 }

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) product_simt_kernel(Product p) {
             }
             if (EPI == EPI_STORE) st_elem(out + m * p.old[z] + n, v[0]);
             if (EPI == EPI_GLU) {
-                st_elem(out + m * p.old[z] + n, silu_f32(v[0]) * v[NB - 1]);
+                st_elem(out + m * p.old[z] + n, silu<false>(v[0]) * v[NB - 1]);
                 if (p.keep[0]) {
                     st_elem(static_cast<float *>(p.keep[0]) + m * p.kld + n, v[0]);
                     st_elem(static_cast<float *>(p.keep[1]) + m * p.kld + n, v[NB - 1]);
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) product_simt_kernel(Product p) {
             }
             if (EPI == EPI_GLU_BWD) {
                 float dg, du;
-                glu_grad(v[0], v[NB - 1], dense::ld_elem(static_cast<const float *>(p.dh) + m * p.dhld + n), dg, du);
+                glu_grad<false>(v[0], v[NB - 1], dense::ld_elem(static_cast<const float *>(p.dh) + m * p.dhld + n), dg, du);
                 st_elem(static_cast<float *>(p.keep[0]) + m * p.kld + n, dg);
                 st_elem(static_cast<float *>(p.keep[1]) + m * p.kld + n, du);
             }
@@ -134,19 +134,52 @@ __global__ void pack_kernel(const T *__restrict__ src, long long ld, uint8_t *__
     }
 }
 
-// dg, du from kept projections: bandwidth bound, one element a thread
-template <typename T>
-__global__ void glu_dgate_kernel(const T *__restrict__ dh, long long dhld, const T *__restrict__ g,
-                                 const T *__restrict__ u, T *__restrict__ dg, T *__restrict__ du, long long ld,
-                                 long long M, long long N) {
-    const long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+// dg, du from kept projections.  Bandwidth bound: three reads and two writes of
+// an element each; VEC: 16 bytes of every array a thread (all rows on 16-byte
+// addresses), else one element.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) glu_dgate_kernel(const T *__restrict__ dh, long long dhld, const T *__restrict__ g,
+                                                        const T *__restrict__ u, T *__restrict__ dg, T *__restrict__ du,
+                                                        long long ld, long long M, long long N) {
+    constexpr int kPer = VEC ? 16 / sizeof(T) : 1;
+    constexpr bool kFast = sizeof(T) == 2;
+    const long long n = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
     if (n >= N) return;
     for (long long m = blockIdx.y; m < M; m += gridDim.y) {
-        float a, b;
-        glu_grad(dense::ld_elem(g + m * N + n), dense::ld_elem(u + m * N + n), dense::ld_elem(dh + m * dhld + n), a, b);
-        st_elem(dg + m * ld + n, a);
-        st_elem(du + m * ld + n, b);
+        alignas(16) T a[kPer], b[kPer], d[kPer];
+        if (VEC) {
+            *reinterpret_cast<uint4 *>(a) = __ldg(reinterpret_cast<const uint4 *>(g + m * N + n));
+            *reinterpret_cast<uint4 *>(b) = __ldg(reinterpret_cast<const uint4 *>(u + m * N + n));
+            *reinterpret_cast<uint4 *>(d) = __ldg(reinterpret_cast<const uint4 *>(dh + m * dhld + n));
+        } else {
+            a[0] = g[m * N + n], b[0] = u[m * N + n], d[0] = dh[m * dhld + n];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            float x, y;
+            glu_grad<kFast>((float)a[i], (float)b[i], (float)d[i], x, y);
+            st_elem(a + i, x);
+            st_elem(b + i, y);
+        }
+        if (VEC) {
+            *reinterpret_cast<uint4 *>(dg + m * ld + n) = *reinterpret_cast<const uint4 *>(a);
+            *reinterpret_cast<uint4 *>(du + m * ld + n) = *reinterpret_cast<const uint4 *>(b);
+        } else {
+            dg[m * ld + n] = a[0], du[m * ld + n] = b[0];
+        }
     }
+}
+template <typename T>
+cudaError_t launch_dgate_t(const T *dh, long long dhld, const T *gu, T *dg, T *du, long long ld, long long M, long long N,
+                           cudaStream_t s) {
+    constexpr int kPer = 16 / sizeof(T);
+    // dg, du: the workspace's aligned planes
+    const bool vec = !((uintptr_t)dh & 15u) && !(dhld % kPer) && !((uintptr_t)gu & 15u) && !(N % kPer);
+    const long long per = vec ? 256 * kPer : 256;
+    const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)(M < 32768 ? M : 32768));
+    if (vec) glu_dgate_kernel<T, true><<<grid, 256, 0, s>>>(dh, dhld, gu, gu + M * N, dg, du, ld, M, N);
+    else glu_dgate_kernel<T, false><<<grid, 256, 0, s>>>(dh, dhld, gu, gu + M * N, dg, du, ld, M, N);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -169,18 +202,12 @@ cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_
 
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,
                              long long M, long long N, int dtype, cudaStream_t s) {
-    const dim3 grid((unsigned)((N + 255) / 256), (unsigned)(M < 32768 ? M : 32768));
-    if (dtype == MOEQ_ACT_F32) {
-        const float *g = static_cast<const float *>(gu);
-        glu_dgate_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float *>(dh), dhld, g, g + M * N,
-                                                     static_cast<float *>(dg), static_cast<float *>(du), ld, M, N);
-    } else {
-        const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(gu);
-        glu_dgate_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-            static_cast<const __nv_bfloat16 *>(dh), dhld, g, g + M * N, static_cast<__nv_bfloat16 *>(dg),
-            static_cast<__nv_bfloat16 *>(du), ld, M, N);
-    }
-    return cudaGetLastError();
+    typedef __nv_bfloat16 B;
+    if (dtype == MOEQ_ACT_F32)
+        return launch_dgate_t(static_cast<const float *>(dh), dhld, static_cast<const float *>(gu),
+                              static_cast<float *>(dg), static_cast<float *>(du), ld, M, N, s);
+    return launch_dgate_t(static_cast<const B *>(dh), dhld, static_cast<const B *>(gu), static_cast<B *>(dg),
+                          static_cast<B *>(du), ld, M, N, s);
 }
 
 }  // namespace dense

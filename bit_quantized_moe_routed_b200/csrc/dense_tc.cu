@@ -235,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         for (int t = pair; t < tiles; t += pairs, ++q) {
             const TileAt at(t, p.mt, p.nt);
             const int b = q & 1;
-            if (!wait_cluster(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag)) break;
+            if (!mbar_wait_abort(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
             tc_fence_after();
             const long long m0 = (long long)at.m * 2 * kTileM + rank * kTileM + quad * 32, n0 = (long long)at.n * kOutN;
             const int rows = (int)min(32LL, p.M - m0);
@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                         store_32x32<O>(stage, u, static_cast<O *>(p.keep[1]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) g[i] = silu_f32(g[i]) * u[i];
+                    for (int i = 0; i < 32; ++i) g[i] = silu<sizeof(O) == 2>(g[i]) * u[i];
                     store_32x32<O>(stage, g, out + m0 * p.old[0] + n, p.old[0], rows, cols, p.vec_out);
                 } else {
                     const O *dh = static_cast<const O *>(p.dh) + (m0 + lane) * p.dhld + n;
@@ -282,14 +282,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const float d = bf16_bits_to_f32(i & 1 ? ww[i >> 1] >> 16 : ww[i >> 1] & 0xFFFFu);
-                                glu_grad(g[8 * j + i], u[8 * j + i], d, g[8 * j + i], u[8 * j + i]);
+                                glu_grad<sizeof(O) == 2>(g[8 * j + i], u[8 * j + i], d, g[8 * j + i], u[8 * j + i]);
                             }
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const float d = lane < rows && i < cols ? ld_elem(dh + i) : 0.f;
-                            glu_grad(g[i], u[i], d, g[i], u[i]);
+                            glu_grad<sizeof(O) == 2>(g[i], u[i], d, g[i], u[i]);
                         }
                     }
                     store_32x32<O>(stage, g, static_cast<O *>(p.keep[0]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
@@ -372,8 +372,12 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Tile width: the one that leaves the pairs idle least.  A tile of 256
-// columns costs about BN + 24 (the fill of the ring and the epilogue's tail).
+// Tile width: 256 columns unless 128 leave the pairs idle less.  A tile of 128
+// columns does half the work of one of 256 in 0.85 of its time when all pairs
+// are busy (measured at 4096 x 4096 x 2048, bf16: 22.6 against 26.5 us a tile;
+// both are fed at 38 to 47 bytes a clock and SM from L2, and the narrow tile
+// needs 1.5 times the bytes per flop), so it pays only when the wide tiles
+// leave more than that share of the pairs without work.
 template <bool I8, bool A_MN, bool B_MN, int EPI, typename O>
 cudaError_t launch_bn(const Product &p, cudaStream_t s) {
     int sms = 0;
@@ -384,7 +388,7 @@ cudaError_t launch_bn(const Product &p, cudaStream_t s) {
     for (int w : {256, 128}) {
         const long long cols = EPI == EPI_STORE ? w : w / 2;
         const long long tiles = (p.M + 255) / 256 * ((p.N + cols - 1) / cols) * p.nbatch;
-        const long long cost = (tiles + sms / 2 - 1) / (sms / 2) * (w + 24);
+        const long long cost = (tiles + sms / 2 - 1) / (sms / 2) * (w == 256 ? 100 : 85);
         if (w == 256 || cost < best) best = cost, bn = w;
     }
     return bn == 256 ? launch_t<I8, A_MN, B_MN, EPI, 256, O>(p, s) : launch_t<I8, A_MN, B_MN, EPI, 128, O>(p, s);

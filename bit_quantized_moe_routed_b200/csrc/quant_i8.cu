@@ -15,43 +15,89 @@
 // whose a leaves the range in which 127 / a and x (127 / a) are normal take
 // f64 for every element.
 //
-// Bound: HBM.  A row is read once (kept in registers between the maximum and
-// the rounding up to kKeep vectors a thread, read again from L2 beyond that)
-// and written once.  Rows of up to 1024 columns take a warp each (no block
-// barrier, eight rows in flight per CTA), longer ones a CTA.
+// Bound: HBM.  A row is read once (its vectors stay in registers, as loaded,
+// between the maximum and the rounding; longer rows are read again from L2)
+// and written once.  Rows of up to 1024 columns take a warp each, up to 4096
+// four warps, longer ones eight.
+#include <type_traits>
+
 #include "dense.cuh"
 
 namespace moeq {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kKeep = 4;   // vectors of 8 elements a thread keeps
+constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
 
-__device__ __forceinline__ void load8(const float *p, float v[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float v[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Eight elements as loaded, and as f32.
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> {
+    uint4 a;
+    static constexpr int kKeep = 4;     // vectors a thread keeps: 16 registers
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = i < 2 ? a.x : (i < 4 ? a.y : (i < 6 ? a.z : a.w));
+        return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
     }
-}
+    // max of |x| as bits (of f32): ordered like the values, NaN above infinity
+    __device__ __forceinline__ uint32_t amax() const {
+        const uint32_t k = 0x7FFF7FFFu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+        return max(m >> 16, m & 0xFFFFu) << 16;
+    }
+};
+template <> struct Vec8<float> {
+    float4 a, b;
+    static constexpr int kKeep = 4;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        const float4 &v = i < 4 ? a : b;
+        return (i & 3) == 0 ? v.x : ((i & 3) == 1 ? v.y : ((i & 3) == 2 ? v.z : v.w));
+    }
+    __device__ __forceinline__ uint32_t amax() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(get(i)) & 0x7FFFFFFFu);
+        return m;
+    }
+};
 
 struct RowScale {
     float a, inv;
     bool wide;   // take f64 for every element
 };
+__device__ __noinline__ int quant_exact(float x, float a) { return (int)rint((double)x * 127.0 / (double)a); }
 __device__ __forceinline__ int quant1(float x, const RowScale &r) {
-    if (!r.wide) {
-        const float t = x * r.inv, q = rintf(t);
-        if (fabsf(fabsf(t - q) - 0.5f) > 1e-4f) return (int)q;
+    const float t = x * r.inv, m = t + kMagic;
+    if (r.wide || fabsf(t - (m - kMagic)) > 0.4999f) return quant_exact(x, r.a);
+    return __float_as_int(m);   // the low byte
+}
+template <typename T>
+__device__ __forceinline__ uint2 quant8(const Vec8<T> &v, const RowScale &r) {
+    uint32_t w[2];
+    float far = r.wide ? 1.f : 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float t = v.get(4 * h + i) * r.inv, mm = t + kMagic;
+            far = fmaxf(far, fabsf(t - (mm - kMagic)));
+            m[i] = __float_as_uint(mm);
+        }
+        w[h] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
     }
-    return (int)rint((double)x * 127.0 / (double)r.a);
+    if (far > 0.4999f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t q = (uint32_t)quant1(v.get(i), r) & 0xFFu;
+            w[i >> 2] = (w[i >> 2] & ~(0xFFu << (8 * (i & 3)))) | (q << (8 * (i & 3)));
+        }
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 // TPR threads per row, VEC: 16-byte aligned rows of x, 8-byte aligned rows of q
@@ -59,40 +105,37 @@ template <typename T, int TPR, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quant_i8_kernel(const T *__restrict__ x, long long ldx, int rows, int cols,
                                                              int8_t *__restrict__ q, long long ldq,
                                                              float *__restrict__ scale) {
+    constexpr int kKeep = Vec8<T>::kKeep, kWarps = TPR / 32;
     __shared__ uint32_t part[kQThreads / 32];
     const int t = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * (kQThreads / TPR) + threadIdx.x / TPR;
     const bool live = row < rows;
     const T *xr = x + (live ? row : 0) * ldx;
-    const int nv = VEC ? cols / 8 : 0;     // whole vectors; the rest by element
-    float keep[kKeep][8];
-    uint32_t m = 0;   // |x| as bits: ordered like the values, NaN above infinity
-    if (live) {
+    const int nv = VEC && live ? cols / 8 : 0;     // whole vectors; the rest by element
+    Vec8<T> keep[kKeep];
+    uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < kKeep; ++j) {
-            const int v = t + j * TPR;
-            if (v < nv) {
-                load8(xr + 8LL * v, keep[j]);
+    for (int j = 0; j < kKeep; ++j)
+        if (t + j * TPR < nv) keep[j].load(xr + 8LL * (t + j * TPR));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(keep[j][i]) & 0x7FFFFFFFu);
-            }
-        }
-        for (int v = t + kKeep * TPR; v < nv; v += TPR) {
-            float e[8];
-            load8(xr + 8LL * v, e);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[i]) & 0x7FFFFFFFu);
-        }
+    for (int j = 0; j < kKeep; ++j)
+        if (t + j * TPR < nv) m = max(m, keep[j].amax());
+    for (int v = t + kKeep * TPR; v < nv; v += TPR) {
+        Vec8<T> e;
+        e.load(xr + 8LL * v);
+        m = max(m, e.amax());
+    }
+    if (live)
         for (int c = 8 * nv + t; c < cols; c += TPR)
             m = max(m, __float_as_uint(dense::ld_elem(xr + c)) & 0x7FFFFFFFu);
-    }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (TPR > 32) {
+    if (kWarps > 1) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
         __syncthreads();
-        m = part[0];
+        const int first = (threadIdx.x / TPR) * kWarps;
+        m = part[first];
 #pragma unroll
-        for (int i = 1; i < kQThreads / 32; ++i) m = max(m, part[i]);
+        for (int i = 1; i < kWarps; ++i) m = max(m, part[first + i]);
     }
     if (!live) return;
     const bool finite = m < 0x7F800000u;
@@ -103,23 +146,15 @@ __global__ void __launch_bounds__(kQThreads) quant_i8_kernel(const T *__restrict
     if (t == 0) scale[row] = finite ? r.a / 127.0f : __uint_as_float(0x7FC00000u);
     const bool zero = !finite || m == 0;
     int8_t *qr = q + row * ldq;
-    auto put8 = [&](int v, const float e[8]) {
-        uint32_t w[2] = {0, 0};
-        if (!zero) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)quant1(e[i], r) & 0xFFu) << (8 * (i & 3));
-        }
-        *reinterpret_cast<uint2 *>(qr + 8LL * v) = make_uint2(w[0], w[1]);
-    };
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
         const int v = t + j * TPR;
-        if (v < nv) put8(v, keep[j]);
+        if (v < nv) *reinterpret_cast<uint2 *>(qr + 8LL * v) = zero ? make_uint2(0, 0) : quant8(keep[j], r);
     }
     for (int v = t + kKeep * TPR; v < nv; v += TPR) {
-        float e[8];
-        load8(xr + 8LL * v, e);
-        put8(v, e);
+        Vec8<T> e;
+        e.load(xr + 8LL * v);
+        *reinterpret_cast<uint2 *>(qr + 8LL * v) = zero ? make_uint2(0, 0) : quant8(e, r);
     }
     for (int c = 8 * nv + t; c < cols; c += TPR) qr[c] = zero ? 0 : (int8_t)quant1(dense::ld_elem(xr + c), r);
 }
@@ -129,14 +164,15 @@ cudaError_t launch(const void *x, int rows, int cols, long long ldx, int8_t *q, 
                    cudaStream_t s) {
     const T *xt = static_cast<const T *>(x);
     const bool vec = !((uintptr_t)x & 15u) && !((ldx * sizeof(T)) & 15u) && !((uintptr_t)q & 7u) && !(ldq & 7);
-    if (cols <= 1024) {
-        const int grid = (rows + kQThreads / 32 - 1) / (kQThreads / 32);
-        if (vec) quant_i8_kernel<T, 32, true><<<grid, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
-        else quant_i8_kernel<T, 32, false><<<grid, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
-    } else {
-        if (vec) quant_i8_kernel<T, kQThreads, true><<<rows, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
-        else quant_i8_kernel<T, kQThreads, false><<<rows, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
-    }
+    auto run = [&](auto tpr) {
+        constexpr int kTpr = decltype(tpr)::value;
+        const int per = kQThreads / kTpr, grid = (rows + per - 1) / per;
+        if (vec) quant_i8_kernel<T, kTpr, true><<<grid, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
+        else quant_i8_kernel<T, kTpr, false><<<grid, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
+    };
+    if (cols <= 1024) run(std::integral_constant<int, 32>{});
+    else if (cols <= 4096) run(std::integral_constant<int, 128>{});
+    else run(std::integral_constant<int, 256>{});
     return cudaGetLastError();
 }
 

@@ -158,9 +158,11 @@ def vq_encode(w, book13, book8=None, gain=None, col_weight=None, stream=None):
     return idx13, idx8
 
 
-def _need(cond, what):
-    if not cond:
-        raise MoeqError(INVALID_ARGUMENT, what)
+# The dense operators are called once a layer and step, some of them for a
+# few microseconds of device work: their wrappers build messages only when
+# they raise.
+def _bad(what):
+    raise MoeqError(INVALID_ARGUMENT, what)
 
 
 def _act(t, what):
@@ -168,61 +170,70 @@ def _act(t, what):
     import torch
     if t.dtype is torch.bfloat16:
         return 1
-    _need(t.dtype is torch.float32, f"{what}: dtype {t.dtype}")
+    if t.dtype is not torch.float32:
+        _bad(f"{what}: dtype {t.dtype}")
     return 0
 
 
-def _ld(t, shape, dtype, dev, what):
+def _ld(t, rows, cols, dtype, dev, what):
     """Row stride of a 2-D cuda tensor with unit column stride, checked
     against the shape, dtype and device it must have."""
-    _need(t.is_cuda and t.get_device() == dev and t.dtype is dtype and tuple(t.shape) == tuple(shape),
-          f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, need {dtype} {tuple(shape)} on cuda:{dev}")
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
+        _bad(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, need {dtype} {(rows, cols)} on cuda:{dev}")
     rs, cs = t.stride()
-    _need(cs == 1 or t.shape[1] <= 1, f"{what}: column stride {cs}")
-    return max(rs, shape[1]) if shape[0] <= 1 else rs
+    if cs != 1 and cols > 1:
+        _bad(f"{what}: column stride {cs}")
+    return rs if rows > 1 else max(rs, cols)
 
 
 def _vec(t, n, dev, what):
     import torch
-    _need(t.is_cuda and t.get_device() == dev and t.dtype is torch.float32 and tuple(t.shape) == (n,)
-          and t.is_contiguous(), f"{what}: need contiguous float32 ({n},) on cuda:{dev}")
+    if t.dtype is not torch.float32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{what}: need contiguous float32 ({n},) on cuda:{dev}")
     return t.data_ptr()
 
 
 def _on_stream(fn):
     """Run a dense operator's wrapper on ``stream``, or on the current stream
     of its first tensor's device: allocations it makes belong to that stream."""
+    name = fn.__name__
+
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         import torch
-        _need(isinstance(first, torch.Tensor) and first.is_cuda, f"{fn.__name__}: a cuda tensor is needed")
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            _bad(f"{name}: a cuda tensor is needed")
+        dev = first.get_device()
         if stream is not None:
-            _need(stream.device == first.device, f"{fn.__name__}: stream on {stream.device}, tensor on {first.device}")
+            if stream.device_index != dev:
+                _bad(f"{name}: stream on {stream.device}, tensor on {first.device}")
             with torch.cuda.stream(stream):
                 return fn(first, *args, _s=stream.cuda_stream, **kw)
-        dev = first.get_device()
         if torch.cuda.current_device() != dev:
             with torch.cuda.device(dev):
                 return fn(first, *args, _s=torch.cuda.current_stream(dev).cuda_stream, **kw)
-        return fn(first, *args, _s=torch.cuda.current_stream(dev).cuda_stream, **kw)
+        return fn(first, *args, _s=torch._C._cuda_getCurrentRawStream(dev), **kw)
     return call
 
 
-def _call(name, ws_name, which, pack, workspace, dev, s):
-    """One call with its workspace: ``pack(pointer, bytes)`` gives the packed
-    arguments.  A missing workspace is allocated on the call's stream."""
-    import torch
-    args = pack(0, 0)
-    n = getattr(_lib, ws_name)(args, which)
-    _need(n >= 0, name)
+def _call(run, query, which, args, layout, workspace, dev, s, name):
+    """One call with its workspace (the last two of the packed arguments).  A
+    missing workspace is allocated on the call's stream."""
+    packed = layout.pack(*args, 0, 0)
+    n = query(packed, which)
     if n:
+        import torch
+        if n < 0:
+            _bad(name)
         if workspace is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
-        _need(workspace.is_cuda and workspace.get_device() == dev and workspace.is_contiguous()
-              and workspace.numel() * workspace.element_size() >= n,
-              f"{name}: workspace of {n} contiguous bytes on cuda:{dev}")
-        args = pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _check(getattr(_lib, name)(args, s), name)
+        elif (workspace.get_device() != dev or not workspace.is_contiguous()
+              or workspace.numel() * workspace.element_size() < n):
+            _bad(f"{name}: workspace of {n} contiguous bytes on cuda:{dev}")
+        packed = layout.pack(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    code = run(packed, s)
+    if code:
+        _check(code, name)
 
 
 @_on_stream
@@ -230,39 +241,41 @@ def quant_i8(x, q=None, scale=None, _s=0):
     """moeq_quant_i8: rows of x (float32 or bfloat16 [M][K], unit column
     stride) to (q int8 [M][K], scale float32 [M]), x ~ q * scale[:, None]."""
     import torch
-    _need(x.dim() == 2, "quant_i8: x is not 2-D")
+    if x.dim() != 2:
+        _bad("quant_i8: x is not 2-D")
     M, K = x.shape
     dev = x.get_device()
     if q is None:
         q = torch.empty((M, K), dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    ldx = _ld(x, (M, K), x.dtype, dev, "quant_i8: x")
-    _check(_lib.moeq_quant_i8(x.data_ptr(), _act(x, "quant_i8: x"), M, K, ldx, q.data_ptr(),
-                              _ld(q, (M, K), torch.int8, dev, "quant_i8: q"), _vec(scale, M, dev, "quant_i8: scale"),
-                              _s), "moeq_quant_i8")
+    _check(_lib.moeq_quant_i8(x.data_ptr(), _act(x, "quant_i8: x"), M, K, _ld(x, M, K, x.dtype, dev, "quant_i8: x"),
+                              q.data_ptr(), _ld(q, M, K, torch.int8, dev, "quant_i8: q"),
+                              _vec(scale, M, dev, "quant_i8: scale"), _s), "moeq_quant_i8")
     return q, scale
 
 
-def _i8(name, n_w, xq, xs, ws, out, dtype, workspace, s):
+def _i8(name, run, n_w, xq, xs, w0, s0, w1, s1, out, dtype, workspace, s):
     import torch
-    _need(xq.dim() == 2 and ws[0][0].dim() == 2, f"{name}: operands are not 2-D")
+    if xq.dim() != 2 or w0.dim() != 2:
+        _bad(f"{name}: operands are not 2-D")
     T, K = xq.shape
-    N = ws[0][0].shape[0]
+    N = w0.shape[0]
     dev = xq.get_device()
+    i8 = torch.int8
     if out is None:
-        _need(dtype in ACT, f"{name}: dtype {dtype!r}")
+        if dtype not in ACT:
+            _bad(f"{name}: dtype {dtype!r}")
         out = torch.empty((T, N), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device=xq.device)
-    act = _act(out, f"{name}: out")
-    ldx = _ld(xq, (T, K), torch.int8, dev, f"{name}: xq")
-    px = _vec(xs, T, dev, f"{name}: xs")
-    w, ld, sc = [0, 0], [0, 0], [0, 0]
-    for i, (wq, s_w) in enumerate(ws):
-        w[i], ld[i] = wq.data_ptr(), _ld(wq, (N, K), torch.int8, dev, f"{name}: weight {i}")
-        sc[i] = _vec(s_w, N, dev, f"{name}: weight scale {i}")
-    ldo = _ld(out, (T, N), out.dtype, dev, f"{name}: out")
-    head = (T, K, N, act, xq.data_ptr(), ldx, px, w[0], w[1], ld[0], ld[1], sc[0], sc[1], out.data_ptr(), ldo)
-    _call("moeq_" + name, "moeq_i8_workspace", n_w, lambda p, n: I8_ARGS.pack(*head, p, n), workspace, dev, s)
+    act = _act(out, name)
+    ldx, px = _ld(xq, T, K, i8, dev, name), _vec(xs, T, dev, name)
+    ld0, p0 = _ld(w0, N, K, i8, dev, name), _vec(s0, N, dev, name)
+    a1 = ld1 = p1 = 0
+    if w1 is not None:
+        a1, ld1, p1 = w1.data_ptr(), _ld(w1, N, K, i8, dev, name), _vec(s1, N, dev, name)
+    _call(run, _lib.moeq_i8_workspace, n_w,
+          (T, K, N, act, xq.data_ptr(), ldx, px, w0.data_ptr(), a1, ld0, ld1, p0, p1, out.data_ptr(),
+           _ld(out, T, N, out.dtype, dev, name)), I8_ARGS, workspace, dev, s, name)
     return out
 
 
@@ -271,28 +284,28 @@ def matmul_i8(xq, xs, wq, ws, out=None, dtype="bf16", workspace=None, _s=0):
     """moeq_matmul_i8: (xq wq^T) xs[:, None] ws with xq int8 [T][K], wq int8
     [N][K], xs float32 [T], ws float32 [N]; [T][N] in ``dtype`` ("bf16" or
     "f32"), or into ``out``."""
-    return _i8("matmul_i8", 1, xq, xs, [(wq, ws)], out, dtype, workspace, _s)
+    return _i8("matmul_i8", _lib.moeq_matmul_i8, 1, xq, xs, wq, ws, None, None, out, dtype, workspace, _s)
 
 
 @_on_stream
 def glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out=None, dtype="bf16", workspace=None, _s=0):
     """moeq_glu_i8: silu(G) * U with G, U the products of xq with the int8
     weights [N][K] of both projections, as matmul_i8."""
-    return _i8("glu_i8", 2, xq, xs, [(w_gate, s_gate), (w_up, s_up)], out, dtype, workspace, _s)
+    return _i8("glu_i8", _lib.moeq_glu_i8, 2, xq, xs, w_gate, s_gate, w_up, s_up, out, dtype, workspace, _s)
 
 
 def _glu_common(x, w_gate, w_up, gu, what):
-    _need(x.dim() == 2 and w_gate.dim() == 2, f"{what}: operands are not 2-D")
+    if x.dim() != 2 or w_gate.dim() != 2:
+        _bad(f"{what}: operands are not 2-D")
     T, H = x.shape
     N = w_gate.shape[0]
     dev, dt = x.get_device(), x.dtype
-    act = _act(x, f"{what}: x")
-    if gu is not None:
-        _need(gu.is_cuda and gu.get_device() == dev and gu.dtype is dt and tuple(gu.shape) == (2, T, N)
-              and gu.is_contiguous(), f"{what}: gu is not a contiguous {dt} {(2, T, N)} on cuda:{dev}")
-    head = (T, H, N, act, x.data_ptr(), _ld(x, (T, H), dt, dev, f"{what}: x"), w_gate.data_ptr(), w_up.data_ptr(),
-            _ld(w_gate, (N, H), dt, dev, f"{what}: w_gate"), _ld(w_up, (N, H), dt, dev, f"{what}: w_up"),
-            gu.data_ptr() if gu is not None else 0)
+    act = _act(x, what)
+    if gu is not None and (gu.dtype is not dt or gu.shape != (2, T, N) or gu.get_device() != dev
+                           or not gu.is_contiguous()):
+        _bad(f"{what}: gu is not a contiguous {dt} {(2, T, N)} on cuda:{dev}")
+    head = (T, H, N, act, x.data_ptr(), _ld(x, T, H, dt, dev, what), w_gate.data_ptr(), w_up.data_ptr(),
+            _ld(w_gate, N, H, dt, dev, what), _ld(w_up, N, H, dt, dev, what), gu.data_ptr() if gu is not None else 0)
     return T, H, N, dev, dt, head
 
 
@@ -302,15 +315,14 @@ def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, _s=0):
     weights [N][H] (float32 or bfloat16, unit column stride).  With ``save``
     (or a ``gu`` buffer [2][T][N]) returns (h, gu) with both projections kept
     for glu_backward."""
-    import torch
     if save and gu is None and x.dim() == 2 and w_gate.dim() == 2:
-        gu = torch.empty((2, x.shape[0], w_gate.shape[0]), dtype=x.dtype, device=x.device)
+        gu = x.new_empty((2, x.shape[0], w_gate.shape[0]))
     T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, "glu")
     if out is None:
-        out = torch.empty((T, N), dtype=dt, device=x.device)
-    ldh = _ld(out, (T, N), dt, dev, "glu: out")
-    rest = (out.data_ptr(), ldh, 0, 0, 0, 0, 0, 0, 0, 0)
-    _call("moeq_glu", "moeq_glu_workspace", 0, lambda p, n: GLU_ARGS.pack(*head, *rest, p, n), workspace, dev, _s)
+        out = x.new_empty((T, N))
+    _call(_lib.moeq_glu, _lib.moeq_glu_workspace, 0,
+          head + (out.data_ptr(), _ld(out, T, N, dt, dev, "glu: out"), 0, 0, 0, 0, 0, 0, 0, 0), GLU_ARGS, workspace,
+          dev, _s, "glu")
     return out if gu is None else (out, gu)
 
 
@@ -321,27 +333,27 @@ def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None
     gradient dh [T][N] of glu's result; ``gu`` as kept by glu, or None to
     compute the projections again.  Gradients left out (``need_dx``,
     ``need_dw``) come back as None."""
-    import torch
-    T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, "glu_backward")
-    _need((dx is None or need_dx) and ((dw_gate is None and dw_up is None) or need_dw),
-          "glu_backward: a buffer for a gradient that is left out")
-    _need(need_dx or need_dw, "glu_backward: no gradient asked for")
-    if need_dx and dx is None:
-        dx = torch.empty((T, H), dtype=dt, device=x.device)
+    what = "glu_backward"
+    T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, what)
+    if not (need_dx or dx is None) or not (need_dw or (dw_gate is None and dw_up is None)):
+        _bad(f"{what}: a buffer for a gradient that is left out")
+    if not (need_dx or need_dw):
+        _bad(f"{what}: no gradient asked for")
+    pdx = lddx = pg = pu = ldg = ldu = 0
+    if need_dx:
+        if dx is None:
+            dx = x.new_empty((T, H))
+        pdx, lddx = dx.data_ptr(), _ld(dx, T, H, dt, dev, what)
     if need_dw:
         if dw_gate is None:
-            dw_gate = torch.empty((N, H), dtype=dt, device=x.device)
+            dw_gate = x.new_empty((N, H))
         if dw_up is None:
-            dw_up = torch.empty((N, H), dtype=dt, device=x.device)
-    rest = [0, 0, dh.data_ptr(), _ld(dh, (T, N), dt, dev, "glu_backward: dh")]
-    rest += [dx.data_ptr(), _ld(dx, (T, H), dt, dev, "glu_backward: dx")] if need_dx else [0, 0]
-    if need_dw:
-        rest += [dw_gate.data_ptr(), dw_up.data_ptr(), _ld(dw_gate, (N, H), dt, dev, "glu_backward: dw_gate"),
-                 _ld(dw_up, (N, H), dt, dev, "glu_backward: dw_up")]
-    else:
-        rest += [0, 0, 0, 0]
-    _call("moeq_glu_backward", "moeq_glu_workspace", 1, lambda p, n: GLU_ARGS.pack(*head, *rest, p, n), workspace,
-          dev, _s)
+            dw_up = x.new_empty((N, H))
+        pg, pu = dw_gate.data_ptr(), dw_up.data_ptr()
+        ldg, ldu = _ld(dw_gate, N, H, dt, dev, what), _ld(dw_up, N, H, dt, dev, what)
+    _call(_lib.moeq_glu_backward, _lib.moeq_glu_workspace, 1,
+          head + (0, 0, dh.data_ptr(), _ld(dh, T, N, dt, dev, what), pdx, lddx, pg, pu, ldg, ldu), GLU_ARGS, workspace,
+          dev, _s, what)
     return dx, dw_gate, dw_up
 
 
