@@ -79,6 +79,10 @@ __device__ __forceinline__ void st_elem(__nv_bfloat16 *p, float v) { *p = __floa
 cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
+// bf16 and int8, at most kStreamRows rows of A, any strides and alignment (dense_stream.cu)
+constexpr int kStreamRows = 16;
+bool stream_supported(const Product &p);
+cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
 // dst (16-byte aligned base and row stride) = src, rows x cols of es-byte elements
 cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_ld, long long rows, long long cols,
                         int es, cudaStream_t s);

@@ -91,7 +91,8 @@ cudaError_t place(const Packed &k, const void *&p, long long &ld, long long rows
     return e;
 }
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
-    return p.in_dtype == MOEQ_ACT_F32 ? launch_product_simt(p, s) : launch_product_tc(p, s);
+    if (p.in_dtype == MOEQ_ACT_F32) return launch_product_simt(p, s);
+    return stream_supported(p) ? launch_product_stream(p, s) : launch_product_tc(p, s);
 }
 
 bool i8_args_ok(const moeq_i8_args *a, int nw) {
@@ -110,7 +111,7 @@ bool i8_args_ok(const moeq_i8_args *a, int nw) {
 }
 Plan plan_i8(const moeq_i8_args *a, int nw) {
     Plan p;
-    if (a->n_tokens == 0) return p;
+    if (a->n_tokens <= kStreamRows) return p;
     p.x = Packed(a->x, a->n_tokens, a->n_in, a->ldx, 1);
     for (int i = 0; i < nw; ++i) p.w[i] = Packed(a->w[i], a->n_out, a->n_in, a->ldw[i], 1);
     return p;
@@ -138,7 +139,7 @@ bool glu_args_ok(const moeq_glu_args *a, bool backward) {
 Plan plan_glu(const moeq_glu_args *a, bool backward) {
     Plan p;
     if (a->n_tokens == 0) return p;
-    if (a->dtype == MOEQ_ACT_BF16) {
+    if (a->dtype == MOEQ_ACT_BF16 && (backward || a->n_tokens > kStreamRows)) {
         if (!backward || !a->gu || a->dw[0]) p.x = Packed(a->x, a->n_tokens, a->hidden, a->ldx, 2);
         if (!backward || !a->gu || a->dx)
             for (int i = 0; i < 2; ++i) p.w[i] = Packed(a->w[i], a->inter, a->hidden, a->ldw[i], 2);
