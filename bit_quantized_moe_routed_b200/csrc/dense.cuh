@@ -80,9 +80,14 @@ cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
 // bf16 and int8, at most kStreamRows rows of A, any strides and alignment (dense_stream.cu)
-constexpr int kStreamRows = 16;
+constexpr int kStreamRows = 8;
 bool stream_supported(const Product &p);
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
+// bf16 and int8, at most kSkinnyRows rows of A; operands as for
+// launch_product_tc (dense_skinny.cu)
+constexpr int kSkinnyRows = 256;
+bool skinny_supported(const Product &p);
+cudaError_t launch_product_skinny(const Product &p, cudaStream_t s);
 // dst (16-byte aligned base and row stride) = src, rows x cols of es-byte elements
 cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_ld, long long rows, long long cols,
                         int es, cudaStream_t s);

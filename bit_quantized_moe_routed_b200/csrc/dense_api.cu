@@ -92,7 +92,8 @@ cudaError_t place(const Packed &k, const void *&p, long long &ld, long long rows
 }
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
     if (p.in_dtype == MOEQ_ACT_F32) return launch_product_simt(p, s);
-    return stream_supported(p) ? launch_product_stream(p, s) : launch_product_tc(p, s);
+    if (stream_supported(p)) return launch_product_stream(p, s);
+    return skinny_supported(p) ? launch_product_skinny(p, s) : launch_product_tc(p, s);
 }
 
 bool i8_args_ok(const moeq_i8_args *a, int nw) {
