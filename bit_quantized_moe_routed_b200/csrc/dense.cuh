@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "async.cuh"
 #include "internal.cuh"
 
 namespace moeq {
@@ -73,6 +74,28 @@ __device__ __forceinline__ float ld_elem(const __nv_bfloat16 *p) {
 }
 __device__ __forceinline__ void st_elem(float *p, float v) { *p = v; }
 __device__ __forceinline__ void st_elem(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Launch as a programmatic dependent of the kernel before it on the stream:
+// the kernel may start while that one drains, and waits for it (pdl_wait_primary)
+// before it touches global memory.  cluster: CTAs of a cluster, 0 for the
+// kernel's own.
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // ---- launchers ----
 // f32, any strides and alignment (dense_simt.cu)

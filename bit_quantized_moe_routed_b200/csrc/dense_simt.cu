@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kThreads) product_simt_kernel(Product p) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) tot[b][i][j] = 0, acc[b][i][j] = 0;
+    pdl_wait_primary();
+    pdl_launch_dependents();
     for (int sgm = 0; sgm < p.nseg; ++sgm) {
         const float *a = static_cast<const float *>(p.a[p.nseg > 1 ? sgm : z]);
         for (long long k0 = 0; k0 < p.K; k0 += kBK) {
@@ -114,8 +116,7 @@ template <int EPI, bool TA, bool TB>
 cudaError_t launch_t(const Product &p, cudaStream_t s) {
     const long long mt = (p.M + kBM - 1) / kBM, nt = (p.N + kBN - 1) / kBN;
     if (mt * p.nbatch > 0x7FFFFFFFLL || nt > 65535) return cudaErrorInvalidConfiguration;
-    product_simt_kernel<EPI, TA, TB><<<dim3((unsigned)(mt * p.nbatch), (unsigned)nt), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(product_simt_kernel<EPI, TA, TB>, dim3((unsigned)(mt * p.nbatch), (unsigned)nt), kThreads, 0, 0, s, p);
 }
 
 // Copy into rows with 16-byte aligned starts: one 16-byte piece a thread
@@ -124,6 +125,8 @@ __global__ void pack_kernel(const T *__restrict__ src, long long ld, uint8_t *__
                             long long rows, long long cols) {
     constexpr int kPer = 16 / sizeof(T);
     const long long c = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
+    pdl_wait_primary();
+    pdl_launch_dependents();
     if (c >= cols) return;
     for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
         const T *p = src + r * ld + c;
@@ -144,6 +147,8 @@ __global__ void __launch_bounds__(256) glu_dgate_kernel(const T *__restrict__ dh
     constexpr int kPer = VEC ? 16 / sizeof(T) : 1;
     constexpr bool kFast = sizeof(T) == 2;
     const long long n = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
+    pdl_wait_primary();
+    pdl_launch_dependents();
     if (n >= N) return;
     for (long long m = blockIdx.y; m < M; m += gridDim.y) {
         alignas(16) T a[kPer], b[kPer], d[kPer];
@@ -177,9 +182,8 @@ cudaError_t launch_dgate_t(const T *dh, long long dhld, const T *gu, T *dg, T *d
     const bool vec = !((uintptr_t)dh & 15u) && !(dhld % kPer) && !((uintptr_t)gu & 15u) && !(N % kPer);
     const long long per = vec ? 256 * kPer : 256;
     const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)(M < 32768 ? M : 32768));
-    if (vec) glu_dgate_kernel<T, true><<<grid, 256, 0, s>>>(dh, dhld, gu, gu + M * N, dg, du, ld, M, N);
-    else glu_dgate_kernel<T, false><<<grid, 256, 0, s>>>(dh, dhld, gu, gu + M * N, dg, du, ld, M, N);
-    return cudaGetLastError();
+    return launch_pdl(vec ? glu_dgate_kernel<T, true> : glu_dgate_kernel<T, false>, grid, 256, 0, 0, s, dh, dhld, gu,
+                      gu + M * N, dg, du, ld, M, N);
 }
 
 }  // namespace
@@ -195,9 +199,10 @@ cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_
     const long long pieces = (cols * es + 15) / 16;
     const dim3 grid((unsigned)((pieces + 127) / 128), (unsigned)(rows < 32768 ? rows : 32768));
     uint8_t *d = static_cast<uint8_t *>(dst);
-    if (es == 1) pack_kernel<int8_t><<<grid, 128, 0, s>>>(static_cast<const int8_t *>(src), ld, d, dst_ld, rows, cols);
-    else pack_kernel<uint16_t><<<grid, 128, 0, s>>>(static_cast<const uint16_t *>(src), ld, d, dst_ld, rows, cols);
-    return cudaGetLastError();
+    if (es == 1)
+        return launch_pdl(pack_kernel<int8_t>, grid, 128, 0, 0, s, static_cast<const int8_t *>(src), ld, d, dst_ld, rows, cols);
+    return launch_pdl(pack_kernel<uint16_t>, grid, 128, 0, 0, s, static_cast<const uint16_t *>(src), ld, d, dst_ld, rows,
+                      cols);
 }
 
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,

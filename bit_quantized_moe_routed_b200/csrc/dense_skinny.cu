@@ -139,12 +139,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
         mbar_init(&done, 1);
         abort_flag = 0;
         mbar_fence_init();
+        pdl_wait_primary();
         while (issued < S && issued < kb1 - kb0) load(issued);   // the ring's first round waits for nothing
     }
     if (warp == 2) tc_alloc(&tmem_slot, cols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait_primary();
+    pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0 && lane == 0) {
@@ -312,18 +315,8 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
             if (dev < 64) ready[dev] = true;
         }
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.ttiles * ((a.N + kRows - 1) / kRows) * a.split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    const dim3 grid((unsigned)(a.ttiles * ((a.N + kRows - 1) / kRows) * a.split));
+    return launch_pdl(kernel, grid, kThreads, smem, a.split, s, a);
 }
 
 }  // namespace

@@ -3,18 +3,18 @@
 //
 // Bound: HBM, the bytes of the weights.  A CTA takes 16 weight rows (8 gate
 // and the 8 up rows of the same outputs for the gated block) over all of K;
-// its warps split K.  A lane loads 16 consecutive bytes of a row, which are
-// the A fragments of two tensor-core steps under a permutation of K that x
+// its warps split K.  A lane loads 32 consecutive bytes of a row, which are
+// the A fragments of four tensor-core steps under a permutation of K that x
 // shares (the sum does not depend on the order of K), so the weights go from
-// HBM to mma.sync without shared memory, kChunk 64-byte blocks (2 kChunk
-// loads of 16 bytes) a lane in flight.  The tokens are the N = 8 columns of
+// HBM to mma.sync without shared memory, kChunk blocks of 128 bytes of K (2
+// kChunk loads of 32 bytes a lane) always in flight.  The tokens are the N = 8 columns of
 // the step.  tcgen05 would need the weights in shared memory first and pads N
 // to its M; at 8 columns the legacy path leaves the tensor cores far from
 // their limit.  A lane ends with the gate and the up sum of the same outputs;
 // the warps' partial sums meet in shared memory in a fixed order.
 //
-// Operands at any address and row stride: rows that do not start on 16 bytes
-// are read in aligned 4-byte words and shifted.
+// Operands at any address and row stride: rows on 32 bytes are read 32 bytes
+// at a time, rows on 16 bytes 16, others in aligned 4-byte words and shifted.
 #include "dense_tc.cuh"
 
 namespace moeq {
@@ -22,7 +22,8 @@ namespace dense {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kChunk = 8;      // 64-byte blocks of K a warp has in flight
+constexpr int kChunk = 4;      // 128-byte blocks of K a warp has in flight
+constexpr int kAhead = 2;      // blocks by which the tokens are loaded ahead
 
 struct StreamArgs {
     const uint8_t *w[2];
@@ -38,24 +39,18 @@ struct StreamArgs {
     long long kld;
 };
 
-// 16 bytes at p, of which `left` (any value) are inside the row; zeros beyond.
-template <bool VEC>
-__device__ __forceinline__ uint4 load16(const uint8_t *p, int left, bool first) {
-    if (left <= 0) return make_uint4(0, 0, 0, 0);
-    if (VEC && left >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
-    uint32_t w[4];
+// 16 bytes at any address p, of which `left` (any value) are inside the row
+// and `before` say whether bytes before p are; zeros beyond.
+__device__ __forceinline__ void load16_any(const uint8_t *p, int left, bool before, uint32_t w[4]) {
     const int off = (int)((uintptr_t)p & 3);
-    if (!VEC && left >= 20 && !(first && off)) {   // whole words of the row around the 16 bytes
+    if (left >= 20 && (before || !off)) {   // whole words of the row around the 16 bytes
         const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-        uint32_t a = __ldg(q);
+        uint32_t v[5];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t b = off ? __ldg(q + i + 1) : 0u;
-            const uint32_t c = off ? b : (i < 3 ? __ldg(q + i + 1) : 0u);
-            w[i] = off ? __funnelshift_r(a, b, 8 * off) : a;
-            a = c;
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 5; ++i) v[i] = __ldg(q + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+        return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -64,7 +59,31 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p, int left, bool first) 
         for (int j = 0; j < 4; ++j)
             if (4 * i + j < left) w[i] |= (uint32_t)__ldg(p + 4 * i + j) << (8 * j);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The 32 bytes a lane takes of a row's 128-byte block.  ALIGN: 32 or 16 (base,
+// row stride and row length are multiples of it, so a piece is inside the row
+// or not) or 0 (anything).
+template <int ALIGN>
+__device__ __forceinline__ void load32(const uint8_t *p, int left, bool before, uint32_t w[8]) {
+    if (ALIGN == 0) {
+        load16_any(p, left, before, w);
+        load16_any(p + 16, left - 16, true, w + 4);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0;
+    if (ALIGN == 32 && left > 0)
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    if (ALIGN == 16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (left > 16 * h) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + h);
+                w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+            }
+    }
 }
 
 template <bool I8> struct Sum { typedef float type; };
@@ -83,11 +102,10 @@ __device__ __forceinline__ void step(int c[4], uint32_t a0, uint32_t a1, uint32_
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: tiles of 8 tokens
-template <bool I8, int EPI, int NT, bool VEC, typename O>
+template <bool I8, int EPI, int ALIGN, typename O>
 __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __grid_constant__ StreamArgs p) {
     typedef typename Sum<I8>::type E;
-    __shared__ E part[kWarps][NT][4][32];
+    __shared__ E part[kWarps][4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int per = EPI == EPI_STORE ? 16 : 8;            // outputs of a group
     const int n0 = blockIdx.x * per;
@@ -96,49 +114,50 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
     const uint8_t *w1 = EPI == EPI_STORE ? p.w[0] + (long long)min(r1, p.N - 1) * p.ldw[0]
                                          : p.w[1] + (long long)min(r1, p.N - 1) * p.ldw[1];
     const int k0 = r0 < p.N ? p.kbytes : 0, k1 = r1 < p.N ? p.kbytes : 0;
-    E c[NT][4];
+    const uint8_t *xp = p.x + (long long)min(g, p.T - 1) * p.ldx;
+    const int kx = g < p.T ? p.kbytes : 0;
+    E c[4] = {0, 0, 0, 0};
+    const int blocks = (p.kbytes + 127) / 128, share = (blocks + kWarps - 1) / kWarps;
+    const int b_first = warp * share, b_end = min(blocks, (warp + 1) * share);
+    uint32_t a[kChunk][2][8], xr[kAhead][8];
+    auto load_w = [&](int j, int b) {
+        const int k = b * 128 + 32 * t;
+        const bool in = b < b_end;
+        load32<ALIGN>(w0 + k, in ? k0 - k : 0, k > 0, a[j][0]);
+        load32<ALIGN>(w1 + k, in ? k1 - k : 0, k > 0, a[j][1]);
+    };
+    auto load_x = [&](int j, int b) {
+        const int k = b * 128 + 32 * t;
+        load32<ALIGN>(xp + k, b < b_end ? kx - k : 0, k > 0, xr[j]);
+    };
+    pdl_wait_primary();
+    pdl_launch_dependents();
 #pragma unroll
-    for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0;
-    const int blocks = (p.kbytes + 63) / 64, share = (blocks + kWarps - 1) / kWarps;
-    const int b_end = min(blocks, (warp + 1) * share);
-    for (int b0 = warp * share; b0 < b_end; b0 += kChunk) {
-        uint4 a[kChunk][2];
+    for (int j = 0; j < kChunk; ++j) load_w(j, b_first + j);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            const int k = (b0 + j) * 64 + 16 * t;
-            const bool in = b0 + j < b_end;
-            a[j][0] = load16<VEC>(w0 + k, in ? k0 - k : 0, k == 0);
-            a[j][1] = load16<VEC>(w1 + k, in ? k1 - k : 0, k == 0);
-        }
+    for (int j = 0; j < kAhead; ++j) load_x(j, b_first + j);
+    for (int b0 = b_first; b0 < b_end; b0 += kChunk) {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            const int k = (b0 + j) * 64 + 16 * t;
-            if (b0 + j >= b_end) break;
+        for (int j = 0; j < kChunk; ++j) {   // a block past the share's end is zeros on both sides
+            const uint32_t *x = xr[j % kAhead];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int tok = 8 * i + g;
-                const uint4 x = load16<VEC>(p.x + (long long)min(tok, p.T - 1) * p.ldx + k, tok < p.T ? p.kbytes - k : 0,
-                                            k == 0);
-                step(c[i], a[j][0].x, a[j][1].x, a[j][0].y, a[j][1].y, x.x, x.y);
-                step(c[i], a[j][0].z, a[j][1].z, a[j][0].w, a[j][1].w, x.z, x.w);
-            }
+            for (int q = 0; q < 8; q += 2) step(c, a[j][0][q], a[j][1][q], a[j][0][q + 1], a[j][1][q + 1], x[q], x[q + 1]);
+            load_w(j, b0 + kChunk + j);
+            load_x(j % kAhead, b0 + kAhead + j);
         }
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) part[warp][i][q][lane] = c[i][q];
+    for (int q = 0; q < 4; ++q) part[warp][q][lane] = c[q];
     __syncthreads();
-    // output o of the group's 8 NT tokens: the lane and component that hold it
-    for (int o = threadIdx.x; o < per * 8 * NT; o += kThreads) {
-        const int r = o % per, tok = o / per, n = n0 + r;
-        if (tok >= p.T || n >= p.N) continue;
-        const int i = tok >> 3, src = (r & 7) * 4 + ((tok & 7) >> 1), q = (tok & 1) + (r >> 3) * 2;
+    // one output a thread: the lane and component that hold its sums
+    const int r = threadIdx.x % per, tok = threadIdx.x / per, n = n0 + r;
+    if (tok < p.T && n < p.N) {
+        const int src = (r & 7) * 4 + (tok >> 1), q = (tok & 1) + (r >> 3) * 2;
         E s0 = 0, s1 = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            s0 += part[w][i][q][src];
-            if (EPI == EPI_GLU) s1 += part[w][i][q + 2][src];
+            s0 += part[w][q][src];
+            if (EPI == EPI_GLU) s1 += part[w][q + 2][src];
         }
         float v0 = (float)s0, v1 = (float)s1;
         if (I8) {
@@ -163,13 +182,14 @@ template <bool I8, int EPI, typename O>
 cudaError_t launch_t(const Product &p, cudaStream_t s) {
     const int es = I8 ? 1 : 2;
     StreamArgs a{};
-    bool vec = !((uintptr_t)p.a[0] & 15u) && !((p.ald * es) & 15);
+    // the alignment that every row of every operand has
+    unsigned long long low = (uintptr_t)p.a[0] | (p.M > 1 ? p.ald * es : 0) | p.K * es;
     for (int i = 0; i < (EPI == EPI_GLU ? 2 : 1); ++i) {
         a.w[i] = static_cast<const uint8_t *>(p.b[i]);
         a.ldw[i] = p.bld[i] * es;
         a.b_scale[i] = p.b_scale[i];
         a.keep[i] = p.keep[i];
-        vec = vec && !((uintptr_t)p.b[i] & 15u) && !(a.ldw[i] & 15);
+        low |= (uintptr_t)p.b[i] | (p.N > 1 ? a.ldw[i] : 0);
     }
     if (EPI == EPI_GLU) a.keep[1] = p.keep[1];
     a.x = static_cast<const uint8_t *>(p.a[0]);
@@ -183,14 +203,10 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     a.kld = p.kld;
     const int per = EPI == EPI_STORE ? 16 : 8;
     const int grid = (a.N + per - 1) / per;
-    if (a.T <= 8) {
-        if (vec) product_stream_kernel<I8, EPI, 1, true, O><<<grid, kThreads, 0, s>>>(a);
-        else product_stream_kernel<I8, EPI, 1, false, O><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (vec) product_stream_kernel<I8, EPI, 2, true, O><<<grid, kThreads, 0, s>>>(a);
-        else product_stream_kernel<I8, EPI, 2, false, O><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    const auto kernel = !(low & 31) ? product_stream_kernel<I8, EPI, 32, O>
+                                    : (!(low & 15) ? product_stream_kernel<I8, EPI, 16, O>
+                                                   : product_stream_kernel<I8, EPI, 0, O>);
+    return launch_pdl(kernel, dim3((unsigned)grid), kThreads, 0, 0, s, a);
 }
 
 }  // namespace

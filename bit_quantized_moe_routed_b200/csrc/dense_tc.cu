@@ -149,6 +149,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    pdl_wait_primary();
+    pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = p.mt * p.nt * p.nbatch;
@@ -368,8 +370,7 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     const long long tiles = (long long)a.mt * a.nt * a.nbatch;
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
     const int pairs = (int)std::min<long long>(tiles, sms / 2);
-    kernel<<<2 * pairs, kThreads, R::kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), kThreads, R::kSmem, 0, s, a);
 }
 
 // Tile width: 256 columns unless 128 leave the pairs idle less.  A tile of 128

@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kQThreads) quant_i8_kernel(const T *__restrict
     const int nv = VEC && live ? cols / 8 : 0;     // whole vectors; the rest by element
     Vec8<T> keep[kKeep];
     uint32_t m = 0;
+    pdl_wait_primary();
+    pdl_launch_dependents();
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
         if (t + j * TPR < nv) keep[j].load(xr + 8LL * (t + j * TPR));
@@ -167,13 +169,12 @@ cudaError_t launch(const void *x, int rows, int cols, long long ldx, int8_t *q, 
     auto run = [&](auto tpr) {
         constexpr int kTpr = decltype(tpr)::value;
         const int per = kQThreads / kTpr, grid = (rows + per - 1) / per;
-        if (vec) quant_i8_kernel<T, kTpr, true><<<grid, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
-        else quant_i8_kernel<T, kTpr, false><<<grid, kQThreads, 0, s>>>(xt, ldx, rows, cols, q, ldq, scale);
+        return dense::launch_pdl(vec ? quant_i8_kernel<T, kTpr, true> : quant_i8_kernel<T, kTpr, false>, dim3((unsigned)grid),
+                                 kQThreads, 0, 0, s, xt, ldx, rows, cols, q, ldq, scale);
     };
-    if (cols <= 1024) run(std::integral_constant<int, 32>{});
-    else if (cols <= 4096) run(std::integral_constant<int, 128>{});
-    else run(std::integral_constant<int, 256>{});
-    return cudaGetLastError();
+    if (cols <= 1024) return run(std::integral_constant<int, 32>{});
+    if (cols <= 4096) return run(std::integral_constant<int, 128>{});
+    return run(std::integral_constant<int, 256>{});
 }
 
 }  // namespace
