@@ -103,7 +103,7 @@ cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
 // bf16 and int8, at most kStreamRows rows of A, any strides and alignment (dense_stream.cu)
-constexpr int kStreamRows = 8;
+constexpr int kStreamRows = 16;
 bool stream_supported(const Product &p);
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
 // bf16 and int8, at most kSkinnyRows rows of A; operands as for

@@ -30,7 +30,7 @@ using namespace umma;
 constexpr int kThreads = 256;
 constexpr int kABytes = kT * kRowBytes;   // 16 KB
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 220 * 1024;
+constexpr int kSmemMax = 108 * 1024;      // two CTAs of an SM: the next kernel's wait beside this one's
 
 struct SkinnyArgs {
     CUtensorMap a[2], b[2];    // weights (gate / up, or segments), tokens (segments)
@@ -139,6 +139,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
         mbar_init(&done, 1);
         abort_flag = 0;
         mbar_fence_init();
+        // weights of the ring's first round on their way to L2 while the kernel before drains
+        for (int c = 0; c < S && c < kb1 - kb0; ++c) {
+            const int kb = kb0 + c, seg = p.nseg > 1 && kb >= p.kblocks, k0 = (seg ? kb - p.kblocks : kb) * kKE;
+            if (EPI != EPI_STORE) {
+                tma_prefetch_2d(&p.a[0], k0, n0);
+                tma_prefetch_2d(&p.a[1], k0, n0);
+            } else if (A_MN) {
+                tma_prefetch_2d(&p.a[seg], n0, k0);
+                tma_prefetch_2d(&p.a[seg], n0 + 64, k0);
+            } else {
+                tma_prefetch_2d(&p.a[seg], k0, n0);
+            }
+        }
         pdl_wait_primary();
         while (issued < S && issued < kb1 - kb0) load(issued);   // the ring's first round waits for nothing
     }
@@ -260,8 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
             }
         }
     }
+    // no CTA leaves while another reads its shared memory; the stores above need no order
     __syncwarp();
-    if (p.split > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
+    if (p.split > 1)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, FLAG_TIMEOUT);
 }
 

@@ -8,13 +8,15 @@
 // shares (the sum does not depend on the order of K), so the weights go from
 // HBM to mma.sync without shared memory, kChunk blocks of 128 bytes of K (2
 // kChunk loads of 32 bytes a lane) always in flight.  The tokens are the N = 8 columns of
-// the step.  tcgen05 would need the weights in shared memory first and pads N
+// a step, two steps for up to 16.  tcgen05 would need the weights in shared memory first and pads N
 // to its M; at 8 columns the legacy path leaves the tensor cores far from
 // their limit.  A lane ends with the gate and the up sum of the same outputs;
 // the warps' partial sums meet in shared memory in a fixed order.
 //
 // Operands at any address and row stride: rows on 32 bytes are read 32 bytes
 // at a time, rows on 16 bytes 16, others in aligned 4-byte words and shifted.
+#include <type_traits>
+
 #include "dense_tc.cuh"
 
 namespace moeq {
@@ -23,7 +25,6 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kChunk = 4;      // 128-byte blocks of K a warp has in flight
-constexpr int kAhead = 2;      // blocks by which the tokens are loaded ahead
 
 struct StreamArgs {
     const uint8_t *w[2];
@@ -86,6 +87,8 @@ __device__ __forceinline__ void load32(const uint8_t *p, int left, bool before, 
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <bool I8> struct Sum { typedef float type; };
 template <> struct Sum<true> { typedef int type; };
 
@@ -102,10 +105,12 @@ __device__ __forceinline__ void step(int c[4], uint32_t a0, uint32_t a1, uint32_
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool I8, int EPI, int ALIGN, typename O>
+// NT: tiles of 8 tokens
+template <bool I8, int EPI, int ALIGN, int NT, typename O>
 __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __grid_constant__ StreamArgs p) {
     typedef typename Sum<I8>::type E;
-    __shared__ E part[kWarps][4][32];
+    __shared__ E part[kWarps][NT][4][32];
+    constexpr int kAhead = NT == 1 ? 2 : 1;               // blocks by which the tokens are loaded ahead
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int per = EPI == EPI_STORE ? 16 : 8;            // outputs of a group
     const int n0 = blockIdx.x * per;
@@ -114,12 +119,12 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
     const uint8_t *w1 = EPI == EPI_STORE ? p.w[0] + (long long)min(r1, p.N - 1) * p.ldw[0]
                                          : p.w[1] + (long long)min(r1, p.N - 1) * p.ldw[1];
     const int k0 = r0 < p.N ? p.kbytes : 0, k1 = r1 < p.N ? p.kbytes : 0;
-    const uint8_t *xp = p.x + (long long)min(g, p.T - 1) * p.ldx;
-    const int kx = g < p.T ? p.kbytes : 0;
-    E c[4] = {0, 0, 0, 0};
+    E c[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0;
     const int blocks = (p.kbytes + 127) / 128, share = (blocks + kWarps - 1) / kWarps;
     const int b_first = warp * share, b_end = min(blocks, (warp + 1) * share);
-    uint32_t a[kChunk][2][8], xr[kAhead][8];
+    uint32_t a[kChunk][2][8], xr[kAhead][NT][8];
     auto load_w = [&](int j, int b) {
         const int k = b * 128 + 32 * t;
         const bool in = b < b_end;
@@ -128,8 +133,18 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
     };
     auto load_x = [&](int j, int b) {
         const int k = b * 128 + 32 * t;
-        load32<ALIGN>(xp + k, b < b_end ? kx - k : 0, k > 0, xr[j]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            load32<ALIGN>(p.x + (long long)min(8 * i + g, p.T - 1) * p.ldx + k,
+                          b < b_end && 8 * i + g < p.T ? p.kbytes - k : 0, k > 0, xr[j][i]);
     };
+    // the first blocks on their way to L2 while the kernel before drains
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+        const int k = (b_first + j) * 128 + 32 * t;
+        if (b_first + j < b_end && k < k0) prefetch_l2(w0 + k);
+        if (b_first + j < b_end && k < k1) prefetch_l2(w1 + k);
+    }
     pdl_wait_primary();
     pdl_launch_dependents();
 #pragma unroll
@@ -139,25 +154,31 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
     for (int b0 = b_first; b0 < b_end; b0 += kChunk) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {   // a block past the share's end is zeros on both sides
-            const uint32_t *x = xr[j % kAhead];
 #pragma unroll
-            for (int q = 0; q < 8; q += 2) step(c, a[j][0][q], a[j][1][q], a[j][0][q + 1], a[j][1][q + 1], x[q], x[q + 1]);
+            for (int i = 0; i < NT; ++i) {
+                const uint32_t *x = xr[j % kAhead][i];
+#pragma unroll
+                for (int q = 0; q < 8; q += 2)
+                    step(c[i], a[j][0][q], a[j][1][q], a[j][0][q + 1], a[j][1][q + 1], x[q], x[q + 1]);
+            }
             load_w(j, b0 + kChunk + j);
             load_x(j % kAhead, b0 + kAhead + j);
         }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) part[warp][q][lane] = c[q];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[warp][i][q][lane] = c[i][q];
     __syncthreads();
     // one output a thread: the lane and component that hold its sums
     const int r = threadIdx.x % per, tok = threadIdx.x / per, n = n0 + r;
     if (tok < p.T && n < p.N) {
-        const int src = (r & 7) * 4 + (tok >> 1), q = (tok & 1) + (r >> 3) * 2;
+        const int i = tok >> 3, src = (r & 7) * 4 + ((tok & 7) >> 1), q = (tok & 1) + (r >> 3) * 2;
         E s0 = 0, s1 = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            s0 += part[w][q][src];
-            if (EPI == EPI_GLU) s1 += part[w][q + 2][src];
+            s0 += part[w][i][q][src];
+            if (EPI == EPI_GLU) s1 += part[w][i][q + 2][src];
         }
         float v0 = (float)s0, v1 = (float)s1;
         if (I8) {
@@ -203,9 +224,13 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     a.kld = p.kld;
     const int per = EPI == EPI_STORE ? 16 : 8;
     const int grid = (a.N + per - 1) / per;
-    const auto kernel = !(low & 31) ? product_stream_kernel<I8, EPI, 32, O>
-                                    : (!(low & 15) ? product_stream_kernel<I8, EPI, 16, O>
-                                                   : product_stream_kernel<I8, EPI, 0, O>);
+    auto pick = [&](auto align) {
+        constexpr int A = decltype(align)::value;
+        return a.T <= 8 ? product_stream_kernel<I8, EPI, A, 1, O> : product_stream_kernel<I8, EPI, A, 2, O>;
+    };
+    const auto kernel = !(low & 31) ? pick(std::integral_constant<int, 32>{})
+                                    : (!(low & 15) ? pick(std::integral_constant<int, 16>{})
+                                                   : pick(std::integral_constant<int, 0>{}));
     return launch_pdl(kernel, dim3((unsigned)grid), kThreads, 0, 0, s, a);
 }
 
