@@ -114,7 +114,8 @@ cudaError_t launch_product_skinny(const Product &p, cudaStream_t s);
 // dst (16-byte aligned base and row stride) = src, rows x cols of es-byte elements
 cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_ld, long long rows, long long cols,
                         int es, cudaStream_t s);
-// Address of the current device's status word (dense_tc.cu).
+// SMs of the current device; address of its status word (dense_tc.cu).
+cudaError_t sm_count(int *n);
 cudaError_t status_word(uint32_t **p);
 // dgu[0/1] (row stride ld) = the gradients of the kept projections gu [2][M][N]
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,

@@ -1,112 +1,181 @@
 // dense_simt.cu -- f32 products of the dense operators (any sizes, strides and
 // alignment), and the elementwise steps around the products.
 //
-// One CTA computes a 64 x 64 tile of out (two of them for the gated block,
-// gate and up, which share A) from 16-deep slices of A and B in shared
-// memory, 4 x 4 outputs a thread.  Sums run over at most 256 products before
-// they are added to the total, so the rounding error of an f32 sum of K terms
-// grows like K / 256 + 256 half-ulps instead of K.
+// Bound: the f32 units (128 fma a clock and SM; fma.rn.f32x2 does two with one
+// instruction, which leaves issue slots for the shared-memory loads).  A CTA
+// of 256 threads computes a tile of 16 TM x 64 outputs (32 gate and the 32 up
+// of the same outputs for the gated block), TM x 4 a thread, from slices of 16
+// along K that are copied into a ring of shared-memory stages (4-byte
+// asynchronous copies: any stride and alignment, transposed on the way).  TM = 8 reads 3 x 16 bytes of shared memory for 32 fma; TM =
+// 4 and 2 give small products more tiles.  Sums run over at most 256 products
+// before they are added to the total: the error of a sum of K terms grows like
+// K / 256 + 256 half-ulps instead of K.
 #include "dense.cuh"
 
 namespace moeq {
 namespace dense {
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kBK = 16, kThreads = 256;
-constexpr int kChunk = 256;
+constexpr int kBN = 64, kBK = 16, kThreads = 256;
+constexpr int kChunk = 256 / kBK;   // slices of a partial sum
+typedef unsigned long long f32x2;
 
-// slice [rows][kBK] of a matrix stored [rows][K] (or [K][rows] if TR) into s[k][row]
-template <bool TR>
-__device__ __forceinline__ void load_slice(float (*s)[kBM + 4], const float *g, long long ld, long long r0, long long rows,
-                                           long long k0, long long K) {
-    for (int i = threadIdx.x; i < kBM * kBK; i += kThreads) {
-        const int r = TR ? i % kBM : i / kBK, k = TR ? i / kBM : i % kBK;
-        const long long gr = r0 + r, gk = k0 + k;
-        float v = 0.f;
-        if (gr < rows && gk < K) v = __ldg(TR ? g + gk * ld + gr : g + gr * ld + gk);
-        s[k][r] = v;
-    }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 twice(float a) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(a));
+    return d;
 }
 
-template <int EPI, bool TA, bool TB>
-__global__ void __launch_bounds__(kThreads) product_simt_kernel(Product p) {
-    constexpr int NB = EPI == EPI_STORE ? 1 : 2;
-    __shared__ float sa[kBK][kBM + 4], sb[NB][kBK][kBN + 4];
-    const long long mt = (p.M + kBM - 1) / kBM;
+__device__ __forceinline__ void copy4(float *dst, const float *src, bool in) {   // zero where !in
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// This thread's elements of a slice [ROWS][kBK] of a matrix stored [rows][K]
+// (or [K][rows] if TR), consecutive threads along the contiguous axis: element
+// i lies i steps from the first, in global and in shared memory.
+template <bool TR, int ROWS>
+struct Slice {
+    static constexpr int kN = ROWS * kBK / kThreads;
+    static constexpr int kRowStep = TR ? 0 : kThreads / kBK, kKStep = TR ? kThreads / ROWS : 0;
+    const float *g = nullptr;
+    long long step = 0, slice = 0;
+    int r = 0, k = 0, rows_in = 0;
+    __device__ __forceinline__ void start(const void *base, long long ld, long long r0, long long rows) {
+        r = TR ? threadIdx.x % ROWS : threadIdx.x / kBK;
+        k = TR ? threadIdx.x / ROWS : threadIdx.x % kBK;
+        rows_in = (int)min((long long)ROWS, rows - r0);
+        // rows outside are not read: their addresses stay inside the first row
+        g = static_cast<const float *>(base) + (TR ? (long long)k * ld + r0 + (r < rows_in ? r : 0)
+                                                   : (r0 + (r < rows_in ? r : 0)) * ld + k);
+        step = TR ? (long long)kKStep * ld : (long long)kRowStep * ld;
+        slice = TR ? (long long)kBK * ld : kBK;
+    }
+    // k_left: columns of K left from the slice's first
+    template <typename F>
+    __device__ __forceinline__ void copy(long long k_left, F dst) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const bool in = r + i * kRowStep < rows_in && k + i * kKStep < k_left;
+            copy4(dst(r + i * kRowStep, k + i * kKStep), in ? g + i * step : g, in);
+        }
+    }
+    __device__ __forceinline__ void next() { g += slice; }
+};
+
+template <int EPI, bool TA, bool TB, int TM>
+__global__ void __launch_bounds__(kThreads, 2) product_simt_kernel(const __grid_constant__ Product p) {
+    constexpr int NB = EPI == EPI_STORE ? 1 : 2, kRows = kBN / NB, BM = 16 * TM;
+    constexpr int kLdA = BM + 4, kLdB = kBN + 4, kStages = TM == 8 ? 3 : 4;
+    __shared__ alignas(16) float sa[kStages][kBK][kLdA], sb[kStages][kBK][kLdB];
+    const long long mt = (p.M + BM - 1) / BM;
     const int z = (int)(blockIdx.x / mt);
-    const long long m0 = (blockIdx.x % mt) * kBM, n0 = (long long)blockIdx.y * kBN;
-    const int tm = (threadIdx.x / 16) * 4, tn = (threadIdx.x % 16) * 4;
-    float tot[NB][4][4], acc[NB][4][4];
+    const long long m0 = (blockIdx.x % mt) * BM, n0 = (long long)blockIdx.y * kRows;
+    const int tm = (threadIdx.x / 16) * TM, tn = threadIdx.x % 16;
+    f32x2 tot[TM / 2][4], acc[TM / 2][4];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int i = 0; i < TM / 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) tot[i][j] = acc[i][j] = 0;
+    Slice<TA, BM> xa;
+    Slice<TB, kRows> xb[NB];
+    const int per = (int)((p.K + kBK - 1) / kBK), slices = per * p.nseg;
+    int loaded = 0;
+    long long k_left = 0;
+    auto load = [&]() {   // the next slice, into its stage; an empty group past the last
+        if (loaded < slices) {
+            if (loaded == 0 || loaded == per) {
+                const int seg = loaded == 0 ? 0 : 1;
+                k_left = p.K;
+                xa.start(p.a[p.nseg > 1 ? seg : z], p.ald, m0, p.M);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) tot[b][i][j] = 0, acc[b][i][j] = 0;
+                for (int b = 0; b < NB; ++b) {
+                    const int bi = NB == 2 ? b : seg;
+                    xb[b].start(p.b[bi], p.bld[bi], n0, p.N);
+                }
+            }
+            const int st = loaded % kStages;
+            xa.copy(k_left, [&](int r, int k) { return &sa[st][k][r]; });
+            xa.next();
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {   // gated block: two gate and two up columns side by side
+                xb[b].copy(k_left, [&](int r, int k) { return &sb[st][k][NB == 1 ? r : (r >> 1) * 4 + 2 * b + (r & 1)]; });
+                xb[b].next();
+            }
+            k_left -= kBK;
+            ++loaded;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     pdl_wait_primary();
     pdl_launch_dependents();
-    for (int sgm = 0; sgm < p.nseg; ++sgm) {
-        const float *a = static_cast<const float *>(p.a[p.nseg > 1 ? sgm : z]);
-        for (long long k0 = 0; k0 < p.K; k0 += kBK) {
-            load_slice<TA>(sa, a, p.ald, m0, p.M, k0, p.K);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int bi = NB == 2 ? b : (p.nseg > 1 ? sgm : 0);
-                load_slice<TB>(sb[b], static_cast<const float *>(p.b[bi]), p.bld[bi], n0, p.N, k0, p.K);
+    for (int i = 0; i < kStages - 1; ++i) load();
+    for (int i = 0; i < slices; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();   // slice i has arrived for all; all are done with slice i - 1's stage
+        load();
+        const int st = i % kStages;
+#pragma unroll
+        for (int k = 0; k < kBK; ++k) {
+            f32x2 av[TM / 2];
+            if (TM >= 4) {
+#pragma unroll
+                for (int q = 0; q < TM / 4; ++q) {
+                    const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sa[st][k][tm + 4 * q]);
+                    av[(2 * q) % (TM / 2)] = w.x;
+                    av[(2 * q + 1) % (TM / 2)] = w.y;
+                }
+            } else {
+                av[0] = *reinterpret_cast<const f32x2 *>(&sa[st][k][tm]);
             }
-            __syncthreads();
+            const float4 bv = *reinterpret_cast<const float4 *>(&sb[st][k][4 * tn]);
+            const f32x2 b2[4] = {twice(bv.x), twice(bv.y), twice(bv.z), twice(bv.w)};
 #pragma unroll
-            for (int k = 0; k < kBK; ++k) {
-                float av[4];
+            for (int q = 0; q < TM / 2; ++q)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) av[i] = sa[k][tm + i];
+                for (int j = 0; j < 4; ++j) acc[q][j] = fma2(av[q], b2[j], acc[q][j]);
+        }
+        if ((i + 1) % kChunk == 0 || i + 1 == slices) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+            for (int q = 0; q < TM / 2; ++q)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float bv = sb[b][k][tn + j];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[b][i][j] += av[i] * bv;
-                    }
-            }
-            __syncthreads();
-            if ((k0 + kBK) % kChunk == 0 || k0 + kBK >= p.K) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) tot[b][i][j] += acc[b][i][j], acc[b][i][j] = 0;
-            }
+                for (int j = 0; j < 4; ++j) tot[q][j] = add2(tot[q][j], acc[q][j]), acc[q][j] = 0;
         }
     }
     float *out = static_cast<float *>(p.out[z]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < TM; ++i) {
         const long long m = m0 + tm + i;
         if (m >= p.M) continue;
+        float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const long long n = n0 + tn + j;
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float((uint32_t)(i & 1 ? tot[i / 2][j] >> 32 : tot[i / 2][j]));
+#pragma unroll
+        for (int j = 0; j < 4 / NB; ++j) {
+            const long long n = n0 + tn * (4 / NB) + j;
             if (n >= p.N) continue;
-            float v[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                v[b] = tot[b][i][j];
-            }
-            if (EPI == EPI_STORE) st_elem(out + m * p.old[z] + n, v[0]);
+            if (EPI == EPI_STORE) out[m * p.old[z] + n] = v[j];
             if (EPI == EPI_GLU) {
-                st_elem(out + m * p.old[z] + n, silu<false>(v[0]) * v[NB - 1]);
+                out[m * p.old[z] + n] = silu<false>(v[j]) * v[2 + (j & 1)];
                 if (p.keep[0]) {
-                    st_elem(static_cast<float *>(p.keep[0]) + m * p.kld + n, v[0]);
-                    st_elem(static_cast<float *>(p.keep[1]) + m * p.kld + n, v[NB - 1]);
+                    static_cast<float *>(p.keep[0])[m * p.kld + n] = v[j];
+                    static_cast<float *>(p.keep[1])[m * p.kld + n] = v[2 + (j & 1)];
                 }
             }
             if (EPI == EPI_GLU_BWD) {
                 float dg, du;
-                glu_grad<false>(v[0], v[NB - 1], dense::ld_elem(static_cast<const float *>(p.dh) + m * p.dhld + n), dg, du);
-                st_elem(static_cast<float *>(p.keep[0]) + m * p.kld + n, dg);
-                st_elem(static_cast<float *>(p.keep[1]) + m * p.kld + n, du);
+                glu_grad<false>(v[j], v[2 + (j & 1)], __ldg(static_cast<const float *>(p.dh) + m * p.dhld + n), dg, du);
+                static_cast<float *>(p.keep[0])[m * p.kld + n] = dg;
+                static_cast<float *>(p.keep[1])[m * p.kld + n] = du;
             }
         }
     }
@@ -114,9 +183,18 @@ __global__ void __launch_bounds__(kThreads) product_simt_kernel(Product p) {
 
 template <int EPI, bool TA, bool TB>
 cudaError_t launch_t(const Product &p, cudaStream_t s) {
-    const long long mt = (p.M + kBM - 1) / kBM, nt = (p.N + kBN - 1) / kBN;
-    if (mt * p.nbatch > 0x7FFFFFFFLL || nt > 65535) return cudaErrorInvalidConfiguration;
-    return launch_pdl(product_simt_kernel<EPI, TA, TB>, dim3((unsigned)(mt * p.nbatch), (unsigned)nt), kThreads, 0, 0, s, p);
+    constexpr int kRows = EPI == EPI_STORE ? kBN : kBN / 2;
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const long long nt = (p.N + kRows - 1) / kRows;
+    auto tiles = [&](int tm) { return (p.M + 16 * tm - 1) / (16 * tm) * p.nbatch * nt; };
+    const int tm = tiles(8) >= sms ? 8 : (tiles(4) >= sms ? 4 : 2);
+    const long long mt = (p.M + 16 * tm - 1) / (16 * tm) * p.nbatch;
+    if (mt > 0x7FFFFFFFLL || nt > 65535) return cudaErrorInvalidConfiguration;
+    const auto kernel = tm == 8 ? product_simt_kernel<EPI, TA, TB, 8>
+                                : (tm == 4 ? product_simt_kernel<EPI, TA, TB, 4> : product_simt_kernel<EPI, TA, TB, 2>);
+    return launch_pdl(kernel, dim3((unsigned)mt, (unsigned)nt), kThreads, 0, 0, s, p);
 }
 
 // Copy into rows with 16-byte aligned starts: one 16-byte piece a thread

@@ -20,7 +20,6 @@ constexpr long long kWaitCycles = 2000000000LL; // limit of every wait between r
 // The base and the row stride are multiples of 16 bytes.
 cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long long cols, long long ld, int es,
                      int box_rows);
-cudaError_t sm_count(int *n);
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
