@@ -160,9 +160,33 @@ def vq_encode(w, book13, book8=None, gain=None, col_weight=None, stream=None):
 
 # The dense operators are called once a layer and step, some of them for a
 # few microseconds of device work: their wrappers build messages only when
-# they raise.
+# they raise, and ask for the workspace's size only when one is needed.
 def _bad(what):
     raise MoeqError(INVALID_ARGUMENT, what)
+
+
+def _enter(t, stream, name):
+    """(device index, raw stream) of a call on the current stream of t's
+    device, which is the current device; or (device index, None): the call is
+    to be made again inside _on(t, stream)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _bad(f"{name}: a cuda tensor is needed")
+    dev = t.get_device()
+    if stream is not None:
+        if stream.device_index != dev:
+            _bad(f"{name}: stream on {stream.device}, tensor on {t.device}")
+        return dev, None
+    if torch._C._cuda_getDevice() != dev:
+        return dev, None
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on(dev, stream):
+    """Context of a call on ``stream`` (or the current stream of device
+    ``dev``): allocations made in it belong to that stream."""
+    import torch
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev)
 
 
 def _act(t, what):
@@ -180,6 +204,8 @@ def _ld(t, rows, cols, dtype, dev, what):
     against the shape, dtype and device it must have."""
     if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
         _bad(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, need {dtype} {(rows, cols)} on cuda:{dev}")
+    if t.is_contiguous():
+        return cols
     rs, cs = t.stride()
     if cs != 1 and cols > 1:
         _bad(f"{what}: column stride {cs}")
@@ -193,148 +219,146 @@ def _vec(t, n, dev, what):
     return t.data_ptr()
 
 
-def _on_stream(fn):
-    """Run a dense operator's wrapper on ``stream``, or on the current stream
-    of its first tensor's device: allocations it makes belong to that stream."""
-    name = fn.__name__
-
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        import torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            _bad(f"{name}: a cuda tensor is needed")
-        dev = first.get_device()
-        if stream is not None:
-            if stream.device_index != dev:
-                _bad(f"{name}: stream on {stream.device}, tensor on {first.device}")
-            with torch.cuda.stream(stream):
-                return fn(first, *args, _s=stream.cuda_stream, **kw)
-        if torch.cuda.current_device() != dev:
-            with torch.cuda.device(dev):
-                return fn(first, *args, _s=torch.cuda.current_stream(dev).cuda_stream, **kw)
-        return fn(first, *args, _s=torch._C._cuda_getCurrentRawStream(dev), **kw)
-    return call
-
-
 def _call(run, query, which, args, layout, workspace, dev, s, name):
-    """One call with its workspace (the last two of the packed arguments).  A
-    missing workspace is allocated on the call's stream."""
-    packed = layout.pack(*args, 0, 0)
-    n = query(packed, which)
-    if n:
+    """One call; ``args`` lacks the workspace's address and size.  Without a
+    workspace the call is tried as it is (a call that lacks one is refused
+    before any work); where one is needed it is allocated on the call's
+    stream."""
+    if workspace is None:
+        code = run(layout.pack(*args, 0, 0), s)
+        if code == OK:
+            return
+        n = query(layout.pack(*args, 0, 0), which) if code == INVALID_ARGUMENT else 0
+        if n <= 0:
+            raise MoeqError(code, name)
         import torch
-        if n < 0:
-            _bad(name)
-        if workspace is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
-        elif (workspace.get_device() != dev or not workspace.is_contiguous()
-              or workspace.numel() * workspace.element_size() < n):
-            _bad(f"{name}: workspace of {n} contiguous bytes on cuda:{dev}")
-        packed = layout.pack(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    code = run(packed, s)
-    if code:
-        _check(code, name)
+        workspace = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad(f"{name}: workspace is not contiguous on cuda:{dev}")
+    _check(run(layout.pack(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size()), s), name)
 
 
-@_on_stream
-def quant_i8(x, q=None, scale=None, _s=0):
+def quant_i8(x, q=None, scale=None, stream=None):
     """moeq_quant_i8: rows of x (float32 or bfloat16 [M][K], unit column
     stride) to (q int8 [M][K], scale float32 [M]), x ~ q * scale[:, None]."""
     import torch
+    dev, s = _enter(x, stream, "quant_i8")
+    if s is None:
+        with _on(dev, stream):
+            return quant_i8(x, q, scale)
     if x.dim() != 2:
         _bad("quant_i8: x is not 2-D")
     M, K = x.shape
-    dev = x.get_device()
     if q is None:
-        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+        ldq = K
+    else:
+        ldq = _ld(q, M, K, torch.int8, dev, "quant_i8: q")
     if scale is None:
         scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(_lib.moeq_quant_i8(x.data_ptr(), _act(x, "quant_i8: x"), M, K, _ld(x, M, K, x.dtype, dev, "quant_i8: x"),
-                              q.data_ptr(), _ld(q, M, K, torch.int8, dev, "quant_i8: q"),
-                              _vec(scale, M, dev, "quant_i8: scale"), _s), "moeq_quant_i8")
+    code = _lib.moeq_quant_i8(x.data_ptr(), _act(x, "quant_i8: x"), M, K, _ld(x, M, K, x.dtype, dev, "quant_i8: x"),
+                              q.data_ptr(), ldq, _vec(scale, M, dev, "quant_i8: scale"), s)
+    if code:
+        _check(code, "moeq_quant_i8")
     return q, scale
 
 
-def _i8(name, run, n_w, xq, xs, w0, s0, w1, s1, out, dtype, workspace, s):
+def _i8(name, run, n_w, xq, xs, w0, s0, w1, s1, out, dtype, workspace, dev, s):
     import torch
     if xq.dim() != 2 or w0.dim() != 2:
         _bad(f"{name}: operands are not 2-D")
     T, K = xq.shape
     N = w0.shape[0]
-    dev = xq.get_device()
     i8 = torch.int8
     if out is None:
         if dtype not in ACT:
             _bad(f"{name}: dtype {dtype!r}")
-        out = torch.empty((T, N), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device=xq.device)
-    act = _act(out, name)
+        act, ldo = ACT[dtype], N
+        out = torch.empty((T, N), dtype=torch.bfloat16 if act else torch.float32, device=xq.device)
+    else:
+        act, ldo = _act(out, name), _ld(out, T, N, out.dtype, dev, name)
     ldx, px = _ld(xq, T, K, i8, dev, name), _vec(xs, T, dev, name)
     ld0, p0 = _ld(w0, N, K, i8, dev, name), _vec(s0, N, dev, name)
     a1 = ld1 = p1 = 0
     if w1 is not None:
         a1, ld1, p1 = w1.data_ptr(), _ld(w1, N, K, i8, dev, name), _vec(s1, N, dev, name)
     _call(run, _lib.moeq_i8_workspace, n_w,
-          (T, K, N, act, xq.data_ptr(), ldx, px, w0.data_ptr(), a1, ld0, ld1, p0, p1, out.data_ptr(),
-           _ld(out, T, N, out.dtype, dev, name)), I8_ARGS, workspace, dev, s, name)
+          (T, K, N, act, xq.data_ptr(), ldx, px, w0.data_ptr(), a1, ld0, ld1, p0, p1, out.data_ptr(), ldo), I8_ARGS,
+          workspace, dev, s, name)
     return out
 
 
-@_on_stream
-def matmul_i8(xq, xs, wq, ws, out=None, dtype="bf16", workspace=None, _s=0):
+def matmul_i8(xq, xs, wq, ws, out=None, dtype="bf16", workspace=None, stream=None):
     """moeq_matmul_i8: (xq wq^T) xs[:, None] ws with xq int8 [T][K], wq int8
     [N][K], xs float32 [T], ws float32 [N]; [T][N] in ``dtype`` ("bf16" or
     "f32"), or into ``out``."""
-    return _i8("matmul_i8", _lib.moeq_matmul_i8, 1, xq, xs, wq, ws, None, None, out, dtype, workspace, _s)
+    dev, s = _enter(xq, stream, "matmul_i8")
+    if s is None:
+        with _on(dev, stream):
+            return matmul_i8(xq, xs, wq, ws, out, dtype, workspace)
+    return _i8("matmul_i8", _lib.moeq_matmul_i8, 1, xq, xs, wq, ws, None, None, out, dtype, workspace, dev, s)
 
 
-@_on_stream
-def glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out=None, dtype="bf16", workspace=None, _s=0):
+def glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out=None, dtype="bf16", workspace=None, stream=None):
     """moeq_glu_i8: silu(G) * U with G, U the products of xq with the int8
     weights [N][K] of both projections, as matmul_i8."""
-    return _i8("glu_i8", _lib.moeq_glu_i8, 2, xq, xs, w_gate, s_gate, w_up, s_up, out, dtype, workspace, _s)
+    dev, s = _enter(xq, stream, "glu_i8")
+    if s is None:
+        with _on(dev, stream):
+            return glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out, dtype, workspace)
+    return _i8("glu_i8", _lib.moeq_glu_i8, 2, xq, xs, w_gate, s_gate, w_up, s_up, out, dtype, workspace, dev, s)
 
 
-def _glu_common(x, w_gate, w_up, gu, what):
+def _glu_common(x, w_gate, w_up, gu, dev, what):
     if x.dim() != 2 or w_gate.dim() != 2:
         _bad(f"{what}: operands are not 2-D")
     T, H = x.shape
     N = w_gate.shape[0]
-    dev, dt = x.get_device(), x.dtype
+    dt = x.dtype
     act = _act(x, what)
-    if gu is not None and (gu.dtype is not dt or gu.shape != (2, T, N) or gu.get_device() != dev
-                           or not gu.is_contiguous()):
-        _bad(f"{what}: gu is not a contiguous {dt} {(2, T, N)} on cuda:{dev}")
-    head = (T, H, N, act, x.data_ptr(), _ld(x, T, H, dt, dev, what), w_gate.data_ptr(), w_up.data_ptr(),
-            _ld(w_gate, N, H, dt, dev, what), _ld(w_up, N, H, dt, dev, what), gu.data_ptr() if gu is not None else 0)
-    return T, H, N, dev, dt, head
+    pgu = 0
+    if gu is not None:
+        if gu.dtype is not dt or gu.shape != (2, T, N) or gu.get_device() != dev or not gu.is_contiguous():
+            _bad(f"{what}: gu is not a contiguous {dt} {(2, T, N)} on cuda:{dev}")
+        pgu = gu.data_ptr()
+    return T, H, N, dt, (T, H, N, act, x.data_ptr(), _ld(x, T, H, dt, dev, what), w_gate.data_ptr(), w_up.data_ptr(),
+                         _ld(w_gate, N, H, dt, dev, what), _ld(w_up, N, H, dt, dev, what), pgu)
 
 
-@_on_stream
-def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, _s=0):
+def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, stream=None):
     """moeq_glu: h = silu(x w_gate^T) * (x w_up^T), [T][N], for x [T][H] and
     weights [N][H] (float32 or bfloat16, unit column stride).  With ``save``
     (or a ``gu`` buffer [2][T][N]) returns (h, gu) with both projections kept
     for glu_backward."""
+    dev, s = _enter(x, stream, "glu")
+    if s is None:
+        with _on(dev, stream):
+            return glu(x, w_gate, w_up, save, out, gu, workspace)
     if save and gu is None and x.dim() == 2 and w_gate.dim() == 2:
         gu = x.new_empty((2, x.shape[0], w_gate.shape[0]))
-    T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, "glu")
+    T, H, N, dt, head = _glu_common(x, w_gate, w_up, gu, dev, "glu")
     if out is None:
-        out = x.new_empty((T, N))
-    _call(_lib.moeq_glu, _lib.moeq_glu_workspace, 0,
-          head + (out.data_ptr(), _ld(out, T, N, dt, dev, "glu: out"), 0, 0, 0, 0, 0, 0, 0, 0), GLU_ARGS, workspace,
-          dev, _s, "glu")
+        out, ldh = x.new_empty((T, N)), N
+    else:
+        ldh = _ld(out, T, N, dt, dev, "glu: out")
+    _call(_lib.moeq_glu, _lib.moeq_glu_workspace, 0, head + (out.data_ptr(), ldh, 0, 0, 0, 0, 0, 0, 0, 0), GLU_ARGS,
+          workspace, dev, s, "glu")
     return out if gu is None else (out, gu)
 
 
-@_on_stream
 def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None, need_dx=True, need_dw=True,
-                 workspace=None, _s=0):
+                 workspace=None, stream=None):
     """moeq_glu_backward: (dx [T][H], dw_gate [N][H], dw_up [N][H]) for the
     gradient dh [T][N] of glu's result; ``gu`` as kept by glu, or None to
     compute the projections again.  Gradients left out (``need_dx``,
     ``need_dw``) come back as None."""
+    import torch
     what = "glu_backward"
-    T, H, N, dev, dt, head = _glu_common(x, w_gate, w_up, gu, what)
+    dev, s = _enter(dh, stream, what)
+    if s is None:
+        with _on(dev, stream):
+            return glu_backward(dh, x, w_gate, w_up, gu, dx, dw_gate, dw_up, need_dx, need_dw, workspace)
+    T, H, N, dt, head = _glu_common(x, w_gate, w_up, gu, dev, what)
     if not (need_dx or dx is None) or not (need_dw or (dw_gate is None and dw_up is None)):
         _bad(f"{what}: a buffer for a gradient that is left out")
     if not (need_dx or need_dw):
@@ -351,9 +375,13 @@ def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None
             dw_up = x.new_empty((N, H))
         pg, pu = dw_gate.data_ptr(), dw_up.data_ptr()
         ldg, ldu = _ld(dw_gate, N, H, dt, dev, what), _ld(dw_up, N, H, dt, dev, what)
-    _call(_lib.moeq_glu_backward, _lib.moeq_glu_workspace, 1,
-          head + (0, 0, dh.data_ptr(), _ld(dh, T, N, dt, dev, what), pdx, lddx, pg, pu, ldg, ldu), GLU_ARGS, workspace,
-          dev, _s, what)
+    args = head + (0, 0, dh.data_ptr(), _ld(dh, T, N, dt, dev, what), pdx, lddx, pg, pu, ldg, ldu)
+    if workspace is None:
+        n = _lib.moeq_glu_workspace(GLU_ARGS.pack(*args, 0, 0), 1)
+        if n < 0:
+            _bad(what)
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _call(_lib.moeq_glu_backward, _lib.moeq_glu_workspace, 1, args, GLU_ARGS, workspace, dev, s, what)
     return dx, dw_gate, dw_up
 
 
