@@ -4,16 +4,22 @@
 //   a = max |x|,  scale = a / 127,  q = rne(127 x / a)
 //
 // The integer is defined on the exact quotient, so that it does not depend on
-// how the quotient is formed.  t = x (127 / a) in f32 is off by at most
-// 127 * 3 * 2^-24 < 2.3e-5 (two roundings of a half ulp each, one of them
-// relative to 127 / a, with the margin of one more), so rint(t) is that
-// integer unless t lies within 1e-4 of a half; there (about one element in
-// 5000, and every exact half) the quotient is formed in f64: 127 x has at
-// most 31 significand bits and the f64 quotient of it by a 24-bit value
-// equals a half exactly when the true one does and otherwise stays on its
-// side of it (they differ by at least 2^-25, f64 rounds at 2^-47).  Rows
-// whose a leaves the range in which 127 / a and x (127 / a) are normal take
-// f64 for every element.
+// how the quotient is formed.
+// bf16: 127 x has 15 significand bits and a 8, so the quotient is a half or at
+// least 1 / 510 away from every half.  t0 = 127 x (1 / a), then t = t0 + (127 x -
+// t0 a) (1 / a) in two fma: t differs from the quotient by 2^-46 of it before
+// its own rounding, so a half comes out exactly and rint(t) is the integer.
+// f32: t = x (127 / a) is off by at most 127 * 3 * 2^-24 < 2.3e-5 (two roundings
+// of half an ulp, with the margin of one more), so rint(t) is the integer
+// unless t lies within 3e-5 of a half h.  There the sign of 127 x - h a decides,
+// exactly: with p = rn(h a) and e = h a - p (one fma, exact), 127 x - p is exact
+// in one fma too (127 x and p agree to within 2^-18, and their difference is a
+// multiple of half an ulp of a or x), so 127 x is above, at or below the half as
+// 127 x - p is above, at or below e.
+// Rows whose a leaves the range in which these products are normal take f64 for
+// every element: 127 x has at most 31 significand bits, and its f64 quotient by
+// a 24-bit value is a half exactly when the true one is and otherwise on the
+// same side of it.
 //
 // Bound: HBM.  A row is read once (its vectors stay in registers, as loaded,
 // between the maximum and the rounding; longer rows are read again from L2)
@@ -66,34 +72,47 @@ template <> struct Vec8<float> {
 };
 
 struct RowScale {
-    float a, inv;
-    bool wide;   // take f64 for every element
+    float a, inv;   // inv: 1 / a (bf16) or 127 / a (f32)
 };
-__device__ __noinline__ int quant_exact(float x, float a) { return (int)rint((double)x * 127.0 / (double)a); }
+constexpr float kSure = 0.49997f;       // |t - rint(t)| up to which rint(t) is sure
+__device__ __forceinline__ int quant_wide(float x, float a) { return (int)rint((double)x * 127.0 / (double)a); }
+// t = x r.inv with |t - rint(t)| > kSure: which side of the half next to t
+__device__ __forceinline__ int quant_half(float x, float t, float a) {
+    const float n = rintf(t), h = n + copysignf(0.5f, t - n);
+    const float p = h * a, e = fmaf(h, a, -p), d = fmaf(x, 127.0f, -p);
+    const int k = (int)floorf(h);
+    return d > e ? k + 1 : (d < e ? k : k + (k & 1));
+}
+// bf16: the quotient, exact where it is a half (see above)
+__device__ __forceinline__ float quotient(float x, const RowScale &r) {
+    const float v = 127.0f * x, t0 = v * r.inv;
+    return fmaf(fmaf(-t0, r.a, v), r.inv, t0);
+}
+template <typename T>
 __device__ __forceinline__ int quant1(float x, const RowScale &r) {
-    const float t = x * r.inv, m = t + kMagic;
-    if (r.wide || fabsf(t - (m - kMagic)) > 0.4999f) return quant_exact(x, r.a);
-    return __float_as_int(m);   // the low byte
+    if (sizeof(T) == 2) return (int)rintf(quotient(x, r));
+    const float t = x * r.inv, n = rintf(t);
+    return fabsf(t - n) > kSure ? quant_half(x, t, r.a) : (int)n;
 }
 template <typename T>
 __device__ __forceinline__ uint2 quant8(const Vec8<T> &v, const RowScale &r) {
     uint32_t w[2];
-    float far = r.wide ? 1.f : 0.f;
+    float far = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t m[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float t = v.get(4 * h + i) * r.inv, mm = t + kMagic;
-            far = fmaxf(far, fabsf(t - (mm - kMagic)));
+            const float x = v.get(4 * h + i), t = sizeof(T) == 2 ? quotient(x, r) : x * r.inv, mm = t + kMagic;
+            if (sizeof(T) == 4) far = fmaxf(far, fabsf(t - (mm - kMagic)));
             m[i] = __float_as_uint(mm);
         }
         w[h] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
     }
-    if (far > 0.4999f) {
+    if (sizeof(T) == 4 && far > kSure) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t q = (uint32_t)quant1(v.get(i), r) & 0xFFu;
+            const uint32_t q = (uint32_t)quant1<T>(v.get(i), r) & 0xFFu;
             w[i >> 2] = (w[i >> 2] & ~(0xFFu << (8 * (i & 3)))) | (q << (8 * (i & 3)));
         }
     }
@@ -143,11 +162,15 @@ __global__ void __launch_bounds__(kQThreads) quant_i8_kernel(const T *__restrict
     const bool finite = m < 0x7F800000u;
     RowScale r;
     r.a = __uint_as_float(m);
-    r.inv = 127.0f / r.a;
-    r.wide = !(r.a > 1e-30f && r.a < 1e36f);
+    r.inv = (sizeof(T) == 2 ? 1.0f : 127.0f) / r.a;
     if (t == 0) scale[row] = finite ? r.a / 127.0f : __uint_as_float(0x7FC00000u);
     const bool zero = !finite || m == 0;
     int8_t *qr = q + row * ldq;
+    if (!zero && !(r.a > 1e-30f && r.a < 1e36f)) {   // products of such a row leave f32's normal range
+#pragma unroll 1
+        for (int c = t; c < cols; c += TPR) qr[c] = (int8_t)quant_wide(dense::ld_elem(xr + c), r.a);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
         const int v = t + j * TPR;
@@ -158,7 +181,7 @@ __global__ void __launch_bounds__(kQThreads) quant_i8_kernel(const T *__restrict
         e.load(xr + 8LL * v);
         *reinterpret_cast<uint2 *>(qr + 8LL * v) = zero ? make_uint2(0, 0) : quant8(e, r);
     }
-    for (int c = 8 * nv + t; c < cols; c += TPR) qr[c] = zero ? 0 : (int8_t)quant1(dense::ld_elem(xr + c), r);
+    for (int c = 8 * nv + t; c < cols; c += TPR) qr[c] = zero ? 0 : (int8_t)quant1<T>(dense::ld_elem(xr + c), r);
 }
 
 template <typename T>
