@@ -38,7 +38,8 @@ constexpr int kTileM = 128;                 // rows of A per SM (a pair: 256)
 constexpr int kABytes = kTileM * kRowBytes; // 16 KB
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
-constexpr int kStageOut = kEpiWarps * 4096;
+constexpr int kScaleBytes = 32 * 4;         // a chunk's int8 channel scales
+constexpr int kStageOut = kEpiWarps * (4096 + kScaleBytes);
 constexpr int kGroupM = 8;
 
 struct TcArgs {
@@ -93,7 +94,7 @@ template <int BN>
 struct Ring {
     static constexpr int kBBytes = BN / 2 * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr int kStages = BN == 256 ? 6 : 7;
     static constexpr size_t kSmem = (size_t)kStages * kStage + kStageOut + 1024;
 };
 
@@ -149,12 +150,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    pdl_wait_primary();
-    pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = p.mt * p.nt * p.nbatch;
     const int kb_total = p.kblocks * p.nseg;
+    // f(dst offset in a stage, map, x, y) for every box of K block kb of a tile
+    auto boxes = [&](const TileAt &at, int kb, auto f) {
+        const int m0 = at.m * 2 * kTileM + (int)rank * kTileM;
+        const int n0 = EPI == EPI_STORE ? at.n * BN + (int)rank * (BN / 2) : at.n * kOutN;
+        const int seg = p.nseg > 1 && kb >= p.kblocks, k0 = (seg ? kb - p.kblocks : kb) * kKE;
+        const CUtensorMap *ma = &p.a[p.nseg > 1 ? seg : at.z];
+        const CUtensorMap *mb = &p.b[EPI == EPI_STORE ? seg : (int)rank];
+        if (A_MN) {
+#pragma unroll
+            for (int j = 0; j < kTileM / 64; ++j) f(j * 8192, ma, m0 + 64 * j, k0);
+        } else {
+            f(0, ma, k0, m0);
+        }
+        if (B_MN) {
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j) f(kABytes + j * 8192, mb, n0 + 64 * j, k0);
+        } else {
+            f(kABytes, mb, k0, n0);
+        }
+    };
+    // the first stages' boxes on their way to L2 while the kernel before drains
+    if (threadIdx.x == 0 && pair < tiles) {
+        const TileAt at(pair, p.mt, p.nt);
+        for (int kb = 0; kb < S && kb < kb_total; ++kb)
+            boxes(at, kb, [&](int, const CUtensorMap *map, int x, int y) { tma_prefetch_2d(map, x, y); });
+    }
+    pdl_wait_primary();
+    pdl_launch_dependents();
 
     if (warp == 0 && lane == 0) {
         // ---- loads: this SM's 128 rows of A and its half of B, into the pair's barrier
@@ -162,31 +189,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         bool ok = true;
         for (int t = pair; ok && t < tiles; t += pairs) {
             const TileAt at(t, p.mt, p.nt);
-            const int m0 = at.m * 2 * kTileM + (int)rank * kTileM;
-            const int n0 = EPI == EPI_STORE ? at.n * BN + (int)rank * (BN / 2) : at.n * kOutN;
             for (int kb = 0; kb < kb_total; ++kb, ++c) {
-                const int s = c % S, seg = p.nseg > 1 && kb >= p.kblocks, k0 = (seg ? kb - p.kblocks : kb) * kKE;
+                const int s = c % S;
                 if (c >= S && !wait_cluster(&empty[s], (uint32_t)((c / S - 1) & 1), &abort_flag)) {
                     ok = false;
                     break;
                 }
                 if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
                 const uint32_t bar = in_cta(&full[s], 0);
-                uint8_t *sa = smem + s * R::kStage, *sb = sa + kABytes;
-                const CUtensorMap *ma = &p.a[p.nseg > 1 ? seg : at.z];
-                const CUtensorMap *mb = &p.b[EPI == EPI_STORE ? seg : (int)rank];
-                if (A_MN) {
-#pragma unroll
-                    for (int j = 0; j < kTileM / 64; ++j) tma_load_pair(sa + j * 8192, ma, m0 + 64 * j, k0, bar);
-                } else {
-                    tma_load_pair(sa, ma, k0, m0, bar);
-                }
-                if (B_MN) {
-#pragma unroll
-                    for (int j = 0; j < BN / 128; ++j) tma_load_pair(sb + j * 8192, mb, n0 + 64 * j, k0, bar);
-                } else {
-                    tma_load_pair(sb, mb, k0, n0, bar);
-                }
+                uint8_t *st = smem + s * R::kStage;
+                boxes(at, kb, [&](int off, const CUtensorMap *map, int x, int y) { tma_load_pair(st + off, map, x, y, bar); });
             }
         }
         // the ring's last stages: consumed before this SM's shared memory goes away
@@ -232,6 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         // ---- epilogue: warp w reads lanes 32 (w % 4).., columns by halves
         const int e = warp - 4, quad = e & 3, half = e >> 2;
         uint8_t *stage = stage_out + e * 4096;
+        float *scales = reinterpret_cast<float *>(stage_out + kEpiWarps * 4096 + e * kScaleBytes);
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         int q = 0;
         for (int t = pair; t < tiles; t += pairs, ++q) {
@@ -253,13 +266,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 tmem_ld_wait();
                 if (rows <= 0 || cols <= 0) continue;
                 float g[32], u[32];
+                if (I8) {   // one load of the channel scales a lane, read back as broadcasts
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (I8) {
-                        const bool in = i < cols;
-                        g[i] = (float)(int)r0[i] * sx * (in ? __ldg(p.b_scale[0] + n + i) : 0.f);
-                        if (EPI != EPI_STORE) u[i] = (float)(int)r1[i] * sx * (in ? __ldg(p.b_scale[1] + n + i) : 0.f);
-                    } else {
+                    for (int h = 0; h < (EPI == EPI_STORE ? 1 : 2); ++h) {
+                        __syncwarp();
+                        scales[lane] = lane < cols ? __ldg(p.b_scale[h] + n + lane) : 0.f;
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (h == 0) g[i] = (float)(int)r0[i] * sx * scales[i];
+                            else u[i] = (float)(int)r1[i] * sx * scales[i];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
                         g[i] = __uint_as_float(r0[i]);
                         if (EPI != EPI_STORE) u[i] = __uint_as_float(r1[i]);
                     }
@@ -305,7 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // ends: every wait above is bounded
+    // the other SM's arrivals and loads have ended too (bounded waits above); the results need no order here
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     tc_fence_after();
     if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, FLAG_TIMEOUT);
     if (warp == 2)
