@@ -75,6 +75,27 @@ __device__ __forceinline__ float ld_elem(const __nv_bfloat16 *p) {
 __device__ __forceinline__ void st_elem(float *p, float v) { *p = v; }
 __device__ __forceinline__ void st_elem(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// 16 bytes at any address p, of which `left` (any value) are inside the row
+// and `before` say whether bytes before p are; zeros beyond.
+__device__ __forceinline__ void load16_any(const uint8_t *p, int left, bool before, uint32_t w[4]) {
+    const int off = (int)((uintptr_t)p & 3);
+    if (left >= 20 && (before || !off)) {   // whole words of the row around the 16 bytes
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
+        uint32_t v[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = __ldg(q + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (4 * i + j < left) w[i] |= (uint32_t)__ldg(p + 4 * i + j) << (8 * j);
+    }
+}
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // the kernel may start while that one drains, and waits for it (pdl_wait_primary)
 // before it touches global memory.  cluster: CTAs of a cluster, 0 for the
@@ -102,6 +123,9 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, int cluste
 cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
+// dx and dW (both weights') in one launch, either of them NULL; bf16, operands
+// as for launch_product_tc
+cudaError_t launch_gradients_tc(const Product *dx, const Product *dw, cudaStream_t s);
 // bf16 and int8, at most kStreamRows rows of A, any strides and alignment (dense_stream.cu)
 constexpr int kStreamRows = 16;
 bool stream_supported(const Product &p);
@@ -111,9 +135,15 @@ cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
 constexpr int kSkinnyRows = 256;
 bool skinny_supported(const Product &p);
 cudaError_t launch_product_skinny(const Product &p, cudaStream_t s);
-// dst (16-byte aligned base and row stride) = src, rows x cols of es-byte elements
-cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_ld, long long rows, long long cols,
-                        int es, cudaStream_t s);
+// dst (16-byte aligned base and row stride) = src, rows x cols of es-byte
+// elements, strides in elements; up to three at once.
+struct Copy {
+    const void *src;
+    long long ld;
+    void *dst;
+    long long dst_ld, rows, cols;
+};
+cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s);
 // SMs of the current device; address of its status word (dense_tc.cu).
 cudaError_t sm_count(int *n);
 cudaError_t status_word(uint32_t **p);

@@ -79,21 +79,44 @@ struct Plan {
     long long dgu_ld = 0;
     size_t total() const { return x.bytes + w[0].bytes + w[1].bytes + dgu; }
 };
-// Where an operand of rows x cols lies for the kernels: itself, or (after
-// this copy) the next part of the workspace.
-cudaError_t place(const Packed &k, const void *&p, long long &ld, long long rows, long long cols, int es, char *&ws,
-                  cudaStream_t s) {
-    if (!k.bytes) return cudaSuccess;
-    const cudaError_t e = launch_pack(p, ld, ws, k.ld, rows, cols, es, s);
-    p = ws;
-    ld = k.ld;
-    ws += k.bytes;
-    return e;
-}
+// The copies of a call's packed operands: add() says where an operand lies for
+// the kernels (itself, or the next part of the workspace), run() makes the
+// copies in one launch.
+struct Packing {
+    char *ws;
+    int es;
+    Copy c[3];
+    int n = 0;
+    Packing(void *workspace, int es_) : ws((char *)workspace), es(es_) {}
+    void add(const Packed &k, const void *&p, long long &ld, long long rows, long long cols) {
+        if (!k.bytes) return;
+        c[n++] = Copy{p, ld, ws, k.ld, rows, cols};
+        p = ws;
+        ld = k.ld;
+        ws += k.bytes;
+    }
+    cudaError_t run(cudaStream_t s) const { return n ? launch_pack(c, n, es, s) : cudaSuccess; }
+};
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
     if (p.in_dtype == MOEQ_ACT_F32) return launch_product_simt(p, s);
     if (stream_supported(p)) return launch_product_stream(p, s);
     return skinny_supported(p) ? launch_product_skinny(p, s) : launch_product_tc(p, s);
+}
+
+cudaError_t launch_gradients(const Product *dx, const Product *dw, cudaStream_t s) {
+    const Product *any = dx ? dx : dw;
+    cudaError_t e = cudaSuccess;
+    if (any->in_dtype == MOEQ_ACT_F32) {
+        if (dx) e = launch_product_simt(*dx, s);
+        if (dw && e == cudaSuccess) e = launch_product_simt(*dw, s);
+        return e;
+    }
+    if (dx && skinny_supported(*dx)) {
+        e = launch_product_skinny(*dx, s);
+        dx = nullptr;
+        if (!dw || e != cudaSuccess) return e;
+    }
+    return launch_gradients_tc(dx, dw, s);
 }
 
 bool i8_args_ok(const moeq_i8_args *a, int nw) {
@@ -184,9 +207,10 @@ moeq_status run_i8(const moeq_i8_args *a, int nw, cudaStream_t s) {
     p.in_dtype = kI8;
     p.out_dtype = a->out_dtype;
     p.epi = nw == 2 ? EPI_GLU : EPI_STORE;
-    char *ws = (char *)a->workspace;
-    cudaError_t e = place(plan.x, p.a[0], p.ald, T, K, 1, ws, s);
-    for (int i = 0; i < nw && e == cudaSuccess; ++i) e = place(plan.w[i], p.b[i], p.bld[i], N, K, 1, ws, s);
+    Packing pk(a->workspace, 1);
+    pk.add(plan.x, p.a[0], p.ald, T, K);
+    for (int i = 0; i < nw; ++i) pk.add(plan.w[i], p.b[i], p.bld[i], N, K);
+    const cudaError_t e = pk.run(s);
     return done(e == cudaSuccess ? launch_product(p, s) : e);
 }
 
@@ -252,9 +276,10 @@ extern "C" moeq_status moeq_glu(const moeq_glu_args *a, void *stream) {
     p.in_dtype = p.out_dtype = a->dtype;
     p.epi = EPI_GLU;
     const cudaStream_t s = (cudaStream_t)stream;
-    char *ws = (char *)a->workspace;
-    cudaError_t e = place(plan.x, p.a[0], p.ald, T, H, es, ws, s);
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = place(plan.w[i], p.b[i], p.bld[i], I, H, es, ws, s);
+    Packing pk(a->workspace, es);
+    pk.add(plan.x, p.a[0], p.ald, T, H);
+    for (int i = 0; i < 2; ++i) pk.add(plan.w[i], p.b[i], p.bld[i], I, H);
+    const cudaError_t e = pk.run(s);
     return done(e == cudaSuccess ? launch_product(p, s) : e);
 }
 
@@ -279,13 +304,14 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         }
         return MOEQ_OK;
     }
-    char *ws = (char *)a->workspace;
     const void *x = a->x, *w[2] = {a->w[0], a->w[1]};
     long long ldx = a->ldx, ldw[2] = {a->ldw[0], a->ldw[1]};
-    cudaError_t e = place(plan.x, x, ldx, T, H, es, ws, s);
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = place(plan.w[i], w[i], ldw[i], I, H, es, ws, s);
+    Packing pk(a->workspace, es);
+    pk.add(plan.x, x, ldx, T, H);
+    for (int i = 0; i < 2; ++i) pk.add(plan.w[i], w[i], ldw[i], I, H);
+    cudaError_t e = pk.run(s);
     if (e != cudaSuccess) return MOEQ_ERR_CUDA;
-    char *dg = ws, *du = dg + (size_t)T * plan.dgu_ld * es;
+    char *dg = pk.ws, *du = dg + (size_t)T * plan.dgu_ld * es;
     if (a->gu) {
         e = launch_glu_dgate(a->dh, a->lddh, a->gu, dg, du, plan.dgu_ld, T, I, a->dtype, s);
     } else {
@@ -308,45 +334,35 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         p.epi = EPI_GLU_BWD;
         e = launch_product(p, s);
     }
-    if (e == cudaSuccess && a->dx) {
-        Product p;   // dx = dg W_gate + du W_up: two segments along the reduction
-        p.M = T;
-        p.N = H;
-        p.K = I;
-        p.nseg = 2;
-        p.a[0] = dg;
-        p.a[1] = du;
-        p.ald = plan.dgu_ld;
-        p.b_t = true;
-        for (int i = 0; i < 2; ++i) {
-            p.b[i] = w[i];
-            p.bld[i] = ldw[i];
-        }
-        p.out[0] = a->dx;
-        p.old[0] = a->lddx;
-        p.in_dtype = p.out_dtype = a->dtype;
-        e = launch_product(p, s);
+    if (e != cudaSuccess) return MOEQ_ERR_CUDA;
+    Product px, pw;
+    // dx = dg W_gate + du W_up: two segments along the reduction
+    px.M = T;
+    px.N = H;
+    px.K = I;
+    px.nseg = 2;
+    px.b_t = true;
+    px.out[0] = a->dx;
+    px.old[0] = a->lddx;
+    // dW_i = d_i^T x: two products of one B
+    pw.M = I;
+    pw.N = H;
+    pw.K = T;
+    pw.nbatch = 2;
+    pw.a_t = pw.b_t = true;
+    pw.b[0] = x;
+    pw.bld[0] = ldx;
+    px.a[0] = pw.a[0] = dg;
+    px.a[1] = pw.a[1] = du;
+    px.ald = pw.ald = plan.dgu_ld;
+    px.in_dtype = px.out_dtype = pw.in_dtype = pw.out_dtype = a->dtype;
+    for (int i = 0; i < 2; ++i) {
+        px.b[i] = w[i];
+        px.bld[i] = ldw[i];
+        pw.out[i] = a->dw[i];
+        pw.old[i] = a->lddw[i];
     }
-    if (e == cudaSuccess && a->dw[0]) {
-        Product p;   // dW_i = d_i^T x: two products of one B
-        p.M = I;
-        p.N = H;
-        p.K = T;
-        p.nbatch = 2;
-        p.a[0] = dg;
-        p.a[1] = du;
-        p.ald = plan.dgu_ld;
-        p.a_t = p.b_t = true;
-        p.b[0] = x;
-        p.bld[0] = ldx;
-        for (int i = 0; i < 2; ++i) {
-            p.out[i] = a->dw[i];
-            p.old[i] = a->lddw[i];
-        }
-        p.in_dtype = p.out_dtype = a->dtype;
-        e = launch_product(p, s);
-    }
-    return done(e);
+    return done(launch_gradients(a->dx ? &px : nullptr, a->dw[0] ? &pw : nullptr, s));
 }
 
 extern "C" moeq_status moeq_dense_status(int32_t clear) {

@@ -10,6 +10,8 @@
 // 4 and 2 give small products more tiles.  Sums run over at most 256 products
 // before they are added to the total: the error of a sum of K terms grows like
 // K / 256 + 256 half-ulps instead of K.
+#include <algorithm>
+
 #include "dense.cuh"
 
 namespace moeq {
@@ -197,21 +199,24 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     return launch_pdl(kernel, dim3((unsigned)mt, (unsigned)nt), kThreads, 0, 0, s, p);
 }
 
-// Copy into rows with 16-byte aligned starts: one 16-byte piece a thread
-template <typename T>
-__global__ void pack_kernel(const T *__restrict__ src, long long ld, uint8_t *__restrict__ dst, long long dst_ld,
-                            long long rows, long long cols) {
-    constexpr int kPer = 16 / sizeof(T);
-    const long long c = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
+// Copies of up to three matrices into rows that start on 16 bytes, 16 bytes a
+// thread, read in aligned words and shifted (bandwidth bound: the matrices once
+// in, once out).
+struct PackArgs {
+    const uint8_t *src[3];
+    uint8_t *dst[3];
+    long long ld[3], dst_ld[3], rows[3];   // bytes
+    int cols[3];                           // bytes
+};
+__global__ void __launch_bounds__(128) pack_kernel(const __grid_constant__ PackArgs p) {
+    const int z = blockIdx.z, c = (blockIdx.x * 128 + threadIdx.x) * 16;
     pdl_wait_primary();
     pdl_launch_dependents();
-    if (c >= cols) return;
-    for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-        const T *p = src + r * ld + c;
-        alignas(16) T v[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = c + i < cols ? __ldg(p + i) : (T)0;
-        *reinterpret_cast<uint4 *>(dst + (r * dst_ld + c) * sizeof(T)) = *reinterpret_cast<const uint4 *>(v);
+    if (c >= p.cols[z]) return;
+    for (long long r = blockIdx.y; r < p.rows[z]; r += gridDim.y) {
+        uint32_t w[4];
+        load16_any(p.src[z] + r * p.ld[z] + c, p.cols[z] - c, c > 0, w);
+        *reinterpret_cast<uint4 *>(p.dst[z] + r * p.dst_ld[z] + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -272,15 +277,20 @@ cudaError_t launch_product_simt(const Product &p, cudaStream_t s) {
     return p.a_t ? launch_t<EPI_STORE, true, true>(p, s) : launch_t<EPI_STORE, false, true>(p, s);
 }
 
-cudaError_t launch_pack(const void *src, long long ld, void *dst, long long dst_ld, long long rows, long long cols,
-                        int es, cudaStream_t s) {
-    const long long pieces = (cols * es + 15) / 16;
-    const dim3 grid((unsigned)((pieces + 127) / 128), (unsigned)(rows < 32768 ? rows : 32768));
-    uint8_t *d = static_cast<uint8_t *>(dst);
-    if (es == 1)
-        return launch_pdl(pack_kernel<int8_t>, grid, 128, 0, 0, s, static_cast<const int8_t *>(src), ld, d, dst_ld, rows, cols);
-    return launch_pdl(pack_kernel<uint16_t>, grid, 128, 0, 0, s, static_cast<const uint16_t *>(src), ld, d, dst_ld, rows,
-                      cols);
+cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s) {
+    PackArgs a{};
+    long long pieces = 1, rows = 1;
+    for (int i = 0; i < n; ++i) {
+        a.src[i] = static_cast<const uint8_t *>(c[i].src);
+        a.dst[i] = static_cast<uint8_t *>(c[i].dst);
+        a.ld[i] = c[i].ld * es;
+        a.dst_ld[i] = c[i].dst_ld * es;
+        a.rows[i] = c[i].rows;
+        a.cols[i] = (int)(c[i].cols * es);
+        pieces = std::max<long long>(pieces, (a.cols[i] + 15) / 16);
+        rows = std::max(rows, std::min<long long>(c[i].rows, 16384));
+    }
+    return launch_pdl(pack_kernel, dim3((unsigned)((pieces + 127) / 128), (unsigned)rows, (unsigned)n), 128, 0, 0, s, a);
 }
 
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,

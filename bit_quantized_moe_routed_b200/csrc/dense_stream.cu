@@ -40,27 +40,6 @@ struct StreamArgs {
     long long kld;
 };
 
-// 16 bytes at any address p, of which `left` (any value) are inside the row
-// and `before` say whether bytes before p are; zeros beyond.
-__device__ __forceinline__ void load16_any(const uint8_t *p, int left, bool before, uint32_t w[4]) {
-    const int off = (int)((uintptr_t)p & 3);
-    if (left >= 20 && (before || !off)) {   // whole words of the row around the 16 bytes
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-        uint32_t v[5];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) v[i] = __ldg(q + i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (4 * i + j < left) w[i] |= (uint32_t)__ldg(p + 4 * i + j) << (8 * j);
-    }
-}
 // The 32 bytes a lane takes of a row's 128-byte block.  ALIGN: 32 or 16 (base,
 // row stride and row length are multiples of it, so a piece is inside the row
 // or not) or 0 (anything).

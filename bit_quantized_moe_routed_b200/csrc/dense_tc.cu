@@ -9,7 +9,7 @@
 // and up sums of the same outputs and the epilogue forms silu(g) u, or the
 // gradients dg, du, without another pass.  dx = dg Wg + du Wu runs its
 // reduction over two segments into one accumulator; dWg and dWu are two
-// batches over one B.
+// batches over one B; the three gradients are one launch.
 //
 // Bound: the tensor cores.  Each K block of 128 bytes (64 bf16, 128 s8) is 16
 // KB of A and BN/2 x 128 bytes of B per SM, loaded by TMA (128-byte swizzle)
@@ -18,13 +18,16 @@
 // loads, warp 1 of the first SM issues the MMAs for both, warps 4..11 run the
 // epilogue of one accumulator while the MMAs fill the other (two of BN columns
 // in tensor memory).  Persistent pairs walk the tiles in groups of 8 tile rows
-// so that the tiles in flight share operands in L2.
+// so that the tiles in flight share operands in L2; the longer tiles of a
+// launch come first and the shorter ones even out what they leave.
 //
 // Every wait is bounded: a role that gives up raises the CTA's abort flag, the
 // kernel drains its copies and MMAs, frees its tensor memory and raises the
 // status word.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <utility>
 
 #include "dense_tc.cuh"
 
@@ -42,20 +45,30 @@ constexpr int kScaleBytes = 32 * 4;         // a chunk's int8 channel scales
 constexpr int kStageOut = kEpiWarps * (4096 + kScaleBytes);
 constexpr int kGroupM = 8;
 
-struct TcArgs {
+// One product, or two of one shape over one B.
+struct TcWork {
     CUtensorMap a[2], b[2];
     long long M, N;
     int kblocks;         // K blocks of one segment
     int nseg, nbatch;
     int mt, nt;          // tiles of one batch
-    const float *a_scale, *b_scale[2];
+    bool a_mn;           // A stored [K][M]
     void *out[2];
     long long old[2];
+    bool vec_out;
+    __host__ __device__ int tiles() const { return mt * nt * nbatch; }
+    __host__ __device__ int kb_total() const { return kblocks * nseg; }
+};
+struct TcArgs {
+    TcWork w[2];         // the longer tiles first
+    int nwork;
+    int extra;           // see TileWalk
+    const float *a_scale, *b_scale[2];
     void *keep[2];
     long long kld;
     const void *dh;
     long long dhld;
-    bool vec_out, vec_keep, vec_dh;
+    bool vec_keep, vec_dh;
     uint32_t *status;
 };
 
@@ -98,21 +111,58 @@ struct Ring {
     static constexpr size_t kSmem = (size_t)kStages * kStage + kStageOut + 1024;
 };
 
-// tile index -> batch, tile row, tile column: groups of kGroupM tile rows, row fastest
-struct TileAt {
-    int z, m, n;
-    __device__ __forceinline__ TileAt(int t, int mt, int nt) {
-        z = t / (mt * nt);
-        t -= z * mt * nt;
-        const int per = kGroupM * nt, g = t / per, first = g * kGroupM;
+// The tiles of one pair.  Work 0 goes round the pairs; the pairs that get one
+// tile less of it take `extra` tiles of work 1 first, then work 1 goes round.
+struct TileWalk {
+    const TcArgs &p;
+    int pair, pairs, n0, r0, t = 0, phase = 0;
+    int work = 0, z = 0, m = 0, n = 0;     // the current tile
+    __device__ __forceinline__ TileWalk(const TcArgs &a, int pair_, int pairs_) : p(a), pair(pair_), pairs(pairs_) {
+        n0 = a.w[0].tiles();
+        r0 = n0 % pairs;
+        t = pair;
+    }
+    __device__ __forceinline__ bool next() {
+        if (phase == 0) {
+            if (t < n0) {
+                set(0, t);
+                t += pairs;
+                return true;
+            }
+            if (p.nwork == 1) return false;
+            phase = 1;
+            t = pair - r0;
+        }
+        const int n1 = p.w[1].tiles(), ahead = r0 ? (pairs - r0) * p.extra : 0;
+        if (phase == 1) {
+            if (t >= 0 && t < min(ahead, n1)) {
+                set(1, t);
+                t += pairs - r0;
+                return true;
+            }
+            phase = 2;
+            t = ahead + pair;
+        }
+        if (t >= n1) return false;
+        set(1, t);
+        t += pairs;
+        return true;
+    }
+    // tile index -> batch, tile row, tile column: groups of kGroupM tile rows, row fastest
+    __device__ __forceinline__ void set(int w, int i) {
+        const int mt = p.w[w].mt, nt = p.w[w].nt;
+        work = w;
+        z = i / (mt * nt);
+        i -= z * mt * nt;
+        const int per = kGroupM * nt, g = i / per, first = g * kGroupM;
         const int rows = min(kGroupM, mt - first);
-        t -= g * per;
-        m = first + t % rows;
-        n = t / rows;
+        i -= g * per;
+        m = first + i % rows;
+        n = i / rows;
     }
 };
 
-template <bool I8, bool A_MN, bool B_MN, int EPI, int BN, typename O>
+template <bool I8, bool B_MN, int EPI, int BN, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product_tc_kernel(const __grid_constant__
                                                                                           TcArgs p) {
     typedef Ring<BN> R;
@@ -152,16 +202,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = p.mt * p.nt * p.nbatch;
-    const int kb_total = p.kblocks * p.nseg;
     // f(dst offset in a stage, map, x, y) for every box of K block kb of a tile
-    auto boxes = [&](const TileAt &at, int kb, auto f) {
+    auto boxes = [&](const TileWalk &at, const TcWork &w, int kb, auto f) {
         const int m0 = at.m * 2 * kTileM + (int)rank * kTileM;
         const int n0 = EPI == EPI_STORE ? at.n * BN + (int)rank * (BN / 2) : at.n * kOutN;
-        const int seg = p.nseg > 1 && kb >= p.kblocks, k0 = (seg ? kb - p.kblocks : kb) * kKE;
-        const CUtensorMap *ma = &p.a[p.nseg > 1 ? seg : at.z];
-        const CUtensorMap *mb = &p.b[EPI == EPI_STORE ? seg : (int)rank];
-        if (A_MN) {
+        const int seg = w.nseg > 1 && kb >= w.kblocks, k0 = (seg ? kb - w.kblocks : kb) * kKE;
+        const CUtensorMap *ma = &w.a[w.nseg > 1 ? seg : at.z];
+        const CUtensorMap *mb = &w.b[EPI == EPI_STORE ? seg : (int)rank];
+        if (B_MN && w.a_mn) {
 #pragma unroll
             for (int j = 0; j < kTileM / 64; ++j) f(j * 8192, ma, m0 + 64 * j, k0);
         } else {
@@ -175,10 +223,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         }
     };
     // the first stages' boxes on their way to L2 while the kernel before drains
-    if (threadIdx.x == 0 && pair < tiles) {
-        const TileAt at(pair, p.mt, p.nt);
-        for (int kb = 0; kb < S && kb < kb_total; ++kb)
-            boxes(at, kb, [&](int, const CUtensorMap *map, int x, int y) { tma_prefetch_2d(map, x, y); });
+    if (threadIdx.x == 0) {
+        TileWalk at(p, pair, pairs);
+        if (at.next())
+            for (int kb = 0; kb < S && kb < p.w[at.work].kb_total(); ++kb)
+                boxes(at, p.w[at.work], kb, [&](int, const CUtensorMap *map, int x, int y) { tma_prefetch_2d(map, x, y); });
     }
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -187,8 +236,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         // ---- loads: this SM's 128 rows of A and its half of B, into the pair's barrier
         int c = 0;
         bool ok = true;
-        for (int t = pair; ok && t < tiles; t += pairs) {
-            const TileAt at(t, p.mt, p.nt);
+        for (TileWalk at(p, pair, pairs); ok && at.next();) {
+            const TcWork &w = p.w[at.work];
+            const int kb_total = w.kb_total();
             for (int kb = 0; kb < kb_total; ++kb, ++c) {
                 const int s = c % S;
                 if (c >= S && !wait_cluster(&empty[s], (uint32_t)((c / S - 1) & 1), &abort_flag)) {
@@ -198,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
                 const uint32_t bar = in_cta(&full[s], 0);
                 uint8_t *st = smem + s * R::kStage;
-                boxes(at, kb, [&](int off, const CUtensorMap *map, int x, int y) { tma_load_pair(st + off, map, x, y, bar); });
+                boxes(at, w, kb, [&](int off, const CUtensorMap *map, int x, int y) { tma_load_pair(st + off, map, x, y, bar); });
             }
         }
         // the ring's last stages: consumed before this SM's shared memory goes away
@@ -210,11 +260,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- MMAs of the pair
-        constexpr uint32_t id = idesc_dense<I8>(2 * kTileM, BN, A_MN, B_MN);
         int c = 0, q = 0;
         bool ok = true;
-        for (int t = pair; ok && t < tiles; t += pairs, ++q) {
-            const int b = q & 1;
+        for (TileWalk at(p, pair, pairs); ok && at.next(); ++q) {
+            const bool a_mn = B_MN && p.w[at.work].a_mn;
+            const int kb_total = p.w[at.work].kb_total(), b = q & 1;
+            const uint32_t id = a_mn ? idesc_dense<I8>(2 * kTileM, BN, true, B_MN) : idesc_dense<I8>(2 * kTileM, BN, false, B_MN);
+            const uint64_t step = a_mn ? 2048 >> 4 : 32 >> 4;
             if (q >= 2 && !wait_cluster(&acc_empty[b], (uint32_t)(((q >> 1) - 1) & 1), &abort_flag)) break;
             tc_fence_after();
             for (int kb = 0; kb < kb_total; ++kb, ++c) {
@@ -225,11 +277,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 }
                 tc_fence_after();
                 const uint8_t *sa = smem + s * R::kStage, *sb = sa + kABytes;
-                const uint64_t da = A_MN ? desc_mn_sw128(sa, 8192) : desc_sw128(sa);
+                const uint64_t da = a_mn ? desc_mn_sw128(sa, 8192) : desc_sw128(sa);
                 const uint64_t db = B_MN ? desc_mn_sw128(sb, 8192) : desc_sw128(sb);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)   // 32 bytes of K each: 16 bf16 or 32 s8
-                    mma_pair<I8>(tmem + b * BN, da + k * (A_MN ? 2048 >> 4 : 32 >> 4),
+                    mma_pair<I8>(tmem + b * BN, da + k * step,
                                  db + k * (B_MN ? 2048 >> 4 : 32 >> 4), id, (kb | k) != 0);
                 commit_pair(&empty[s]);
             }
@@ -247,19 +299,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         float *scales = reinterpret_cast<float *>(stage_out + kEpiWarps * 4096 + e * kScaleBytes);
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         int q = 0;
-        for (int t = pair; t < tiles; t += pairs, ++q) {
-            const TileAt at(t, p.mt, p.nt);
+        for (TileWalk at(p, pair, pairs); at.next(); ++q) {
+            const TcWork &w = p.w[at.work];
             const int b = q & 1;
             if (!mbar_wait_abort(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
             tc_fence_after();
             const long long m0 = (long long)at.m * 2 * kTileM + rank * kTileM + quad * 32, n0 = (long long)at.n * kOutN;
-            const int rows = (int)min(32LL, p.M - m0);
+            const int rows = (int)min(32LL, w.M - m0);
             const float sx = I8 && lane < rows ? __ldg(p.a_scale + m0 + lane) : 0.f;
-            O *out = static_cast<O *>(p.out[at.z]);
+            O *out = static_cast<O *>(w.out[at.z]);
 #pragma unroll 1
             for (int c0 = half * (kOutN / 2); c0 < (half + 1) * (kOutN / 2); c0 += 32) {
                 const long long n = n0 + c0;
-                const int cols = (int)max(0LL, min(32LL, p.N - n));
+                const int cols = (int)max(0LL, min(32LL, w.N - n));
                 uint32_t r0[32], r1[32];
                 tmem_ld32(lane_base + b * BN + c0, r0);
                 if (EPI != EPI_STORE) tmem_ld32(lane_base + b * BN + BN / 2 + c0, r1);
@@ -286,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     }
                 }
                 if (EPI == EPI_STORE) {
-                    store_32x32<O>(stage, g, out + m0 * p.old[at.z] + n, p.old[at.z], rows, cols, p.vec_out);
+                    store_32x32<O>(stage, g, out + m0 * w.old[at.z] + n, w.old[at.z], rows, cols, w.vec_out);
                 } else if (EPI == EPI_GLU) {
                     if (!I8 && p.keep[0]) {
                         store_32x32<O>(stage, g, static_cast<O *>(p.keep[0]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
@@ -294,26 +346,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) g[i] = silu<sizeof(O) == 2>(g[i]) * u[i];
-                    store_32x32<O>(stage, g, out + m0 * p.old[0] + n, p.old[0], rows, cols, p.vec_out);
+                    store_32x32<O>(stage, g, out + m0 * w.old[0] + n, w.old[0], rows, cols, w.vec_out);
                 } else {
-                    const O *dh = static_cast<const O *>(p.dh) + (m0 + lane) * p.dhld + n;
-                    if (p.vec_dh && cols == 32 && lane < rows && sizeof(O) == 2) {
+                    if constexpr (sizeof(O) == 2) {
+                        float d[32];
+                        load_32x32(stage, d, static_cast<const O *>(p.dh) + m0 * p.dhld + n, p.dhld, rows, cols, p.vec_dh);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(dh) + j);
-                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float d = bf16_bits_to_f32(i & 1 ? ww[i >> 1] >> 16 : ww[i >> 1] & 0xFFFFu);
-                                glu_grad<sizeof(O) == 2>(g[8 * j + i], u[8 * j + i], d, g[8 * j + i], u[8 * j + i]);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float d = lane < rows && i < cols ? ld_elem(dh + i) : 0.f;
-                            glu_grad<sizeof(O) == 2>(g[i], u[i], d, g[i], u[i]);
-                        }
+                        for (int i = 0; i < 32; ++i) glu_grad<true>(g[i], u[i], d[i], g[i], u[i]);
                     }
                     store_32x32<O>(stage, g, static_cast<O *>(p.keep[0]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
                     store_32x32<O>(stage, u, static_cast<O *>(p.keep[1]) + m0 * p.kld + n, p.kld, rows, cols, p.vec_keep);
@@ -334,36 +373,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
 }
 
-template <bool I8, bool A_MN, bool B_MN, int EPI, int BN, typename O>
-cudaError_t launch_t(const Product &p, cudaStream_t s) {
-    constexpr int kKE = I8 ? 128 : 64, es = I8 ? 1 : 2;
+template <bool I8, bool B_MN, int EPI, int BN, typename O>
+cudaError_t launch_t(const Product *ps, int n, int sms, cudaStream_t s) {
+    constexpr int kKE = I8 ? 128 : 64, es = I8 ? 1 : 2, so = (int)sizeof(O);
     constexpr int kOutN = EPI == EPI_STORE ? BN : BN / 2;
     typedef Ring<BN> R;
     TcArgs a{};
     cudaError_t e = cudaSuccess;
-    const int na = p.nseg > 1 || p.nbatch > 1 ? 2 : 1, nb = EPI == EPI_STORE ? p.nseg : 2;
-    for (int i = 0; i < na && e == cudaSuccess; ++i)
-        e = A_MN ? make_map(&a.a[i], p.a[i], p.K, p.M, p.ald, es, 64)
-                 : make_map(&a.a[i], p.a[i], p.M, p.K, p.ald, es, kTileM);
-    for (int i = 0; i < nb && e == cudaSuccess; ++i)
-        e = B_MN ? make_map(&a.b[i], p.b[i], p.K, p.N, p.bld[i], es, 64)
-                 : make_map(&a.b[i], p.b[i], p.N, p.K, p.bld[i], es, BN / 2);
-    if (e != cudaSuccess) return e;
-    a.M = p.M;
-    a.N = p.N;
-    a.kblocks = (int)((p.K + kKE - 1) / kKE);
-    a.nseg = p.nseg;
-    a.nbatch = p.nbatch;
-    a.mt = (int)((p.M + 2 * kTileM - 1) / (2 * kTileM));
-    a.nt = (int)((p.N + kOutN - 1) / kOutN);
-    const int so = (int)sizeof(O);
-    a.vec_out = true;
+    a.nwork = n;
+    for (int j = 0; j < n; ++j) {
+        const Product &p = ps[j];
+        TcWork &w = a.w[j];
+        w.a_mn = p.a_t;
+        const int na = p.nseg > 1 || p.nbatch > 1 ? 2 : 1, nb = EPI == EPI_STORE ? p.nseg : 2;
+        for (int i = 0; i < na && e == cudaSuccess; ++i)
+            e = p.a_t ? make_map(&w.a[i], p.a[i], p.K, p.M, p.ald, es, 64)
+                      : make_map(&w.a[i], p.a[i], p.M, p.K, p.ald, es, kTileM);
+        for (int i = 0; i < nb && e == cudaSuccess; ++i)
+            e = B_MN ? make_map(&w.b[i], p.b[i], p.K, p.N, p.bld[i], es, 64)
+                     : make_map(&w.b[i], p.b[i], p.N, p.K, p.bld[i], es, BN / 2);
+        if (e != cudaSuccess) return e;
+        w.M = p.M;
+        w.N = p.N;
+        w.kblocks = (int)((p.K + kKE - 1) / kKE);
+        w.nseg = p.nseg;
+        w.nbatch = p.nbatch;
+        w.mt = (int)((p.M + 2 * kTileM - 1) / (2 * kTileM));
+        w.nt = (int)((p.N + kOutN - 1) / kOutN);
+        w.vec_out = true;
+        for (int i = 0; i < 2; ++i) {
+            w.out[i] = p.out[i];
+            w.old[i] = p.old[i];
+            if (p.out[i] && (((uintptr_t)p.out[i] & 15u) || (p.old[i] * so & 15))) w.vec_out = false;
+        }
+        if ((long long)w.mt * w.nt * w.nbatch > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
+    }
+    const Product &p = ps[0];
     for (int i = 0; i < 2; ++i) {
         a.b_scale[i] = p.b_scale[i];
-        a.out[i] = p.out[i];
-        a.old[i] = p.old[i];
         a.keep[i] = p.keep[i];
-        if (p.out[i] && (((uintptr_t)p.out[i] & 15u) || (p.old[i] * so & 15))) a.vec_out = false;
     }
     a.a_scale = p.a_scale;
     a.kld = p.kld;
@@ -371,11 +419,14 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     a.dhld = p.dhld;
     a.vec_keep = !((uintptr_t)p.keep[0] & 15u) && !((uintptr_t)p.keep[1] & 15u) && !(p.kld * so & 15);
     a.vec_dh = !((uintptr_t)p.dh & 15u) && !(p.dhld * so & 15);
-    int sms = 0;
+    long long tiles = a.w[0].tiles();
+    if (n > 1) {
+        tiles += a.w[1].tiles();
+        a.extra = a.w[0].kb_total() / a.w[1].kb_total();
+    }
     e = status_word(&a.status);
-    if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const auto kernel = product_tc_kernel<I8, A_MN, B_MN, EPI, BN, O>;
+    const auto kernel = product_tc_kernel<I8, B_MN, EPI, BN, O>;
     {
         static std::mutex mu;
         static bool ready[64] = {};
@@ -389,8 +440,6 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
             if (dev < 64) ready[dev] = true;
         }
     }
-    const long long tiles = (long long)a.mt * a.nt * a.nbatch;
-    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
     const int pairs = (int)std::min<long long>(tiles, sms / 2);
     return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), kThreads, R::kSmem, 0, s, a);
 }
@@ -401,20 +450,26 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
 // both are fed at 38 to 47 bytes a clock and SM from L2, and the narrow tile
 // needs 1.5 times the bytes per flop), so it pays only when the wide tiles
 // leave more than that share of the pairs without work.
-template <bool I8, bool A_MN, bool B_MN, int EPI, typename O>
-cudaError_t launch_bn(const Product &p, cudaStream_t s) {
+template <bool I8, bool B_MN, int EPI, typename O>
+cudaError_t launch_bn(const Product *ps, int n, cudaStream_t s) {
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    long long best = 0;
-    int bn = 256;
-    for (int w : {256, 128}) {
-        const long long cols = EPI == EPI_STORE ? w : w / 2;
-        const long long tiles = (p.M + 255) / 256 * ((p.N + cols - 1) / cols) * p.nbatch;
-        const long long cost = (tiles + sms / 2 - 1) / (sms / 2) * (w == 256 ? 100 : 85);
-        if (w == 256 || cost < best) best = cost, bn = w;
+    const long long pairs = sms / 2;
+    long long cost[2];
+    for (int h = 0; h < 2; ++h) {
+        const long long cols = (EPI == EPI_STORE ? 256 : 128) >> h;
+        long long work = 0, longest = 0;      // in K blocks: of all tiles, of the longest round
+        for (int j = 0; j < n; ++j) {
+            const long long t = (ps[j].M + 255) / 256 * ((ps[j].N + cols - 1) / cols) * ps[j].nbatch;
+            const long long kb = (ps[j].K + 63) / 64 * ps[j].nseg;
+            work += t * kb;
+            longest = std::max(longest, (t + pairs - 1) / pairs * kb);
+        }
+        const long long kb1 = (ps[n - 1].K + 63) / 64 * ps[n - 1].nseg;
+        cost[h] = std::max(longest, (work + pairs * kb1 - 1) / (pairs * kb1) * kb1) * (h ? 85 : 100);
     }
-    return bn == 256 ? launch_t<I8, A_MN, B_MN, EPI, 256, O>(p, s) : launch_t<I8, A_MN, B_MN, EPI, 128, O>(p, s);
+    return cost[0] <= cost[1] ? launch_t<I8, B_MN, EPI, 256, O>(ps, n, sms, s) : launch_t<I8, B_MN, EPI, 128, O>(ps, n, sms, s);
 }
 
 __device__ uint32_t g_status;
@@ -482,17 +537,25 @@ cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long lo
 }
 
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s) {
+    typedef __nv_bfloat16 B;
     if (p.in_dtype == kI8) {
         if (p.epi == EPI_GLU)
-            return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, false, EPI_GLU, float>(p, s)
-                                               : launch_bn<true, false, false, EPI_GLU, __nv_bfloat16>(p, s);
-        return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, false, EPI_STORE, float>(p, s)
-                                           : launch_bn<true, false, false, EPI_STORE, __nv_bfloat16>(p, s);
+            return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, EPI_GLU, float>(&p, 1, s)
+                                               : launch_bn<true, false, EPI_GLU, B>(&p, 1, s);
+        return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, EPI_STORE, float>(&p, 1, s)
+                                           : launch_bn<true, false, EPI_STORE, B>(&p, 1, s);
     }
-    if (p.epi == EPI_GLU) return launch_bn<false, false, false, EPI_GLU, __nv_bfloat16>(p, s);
-    if (p.epi == EPI_GLU_BWD) return launch_bn<false, false, false, EPI_GLU_BWD, __nv_bfloat16>(p, s);
-    if (p.a_t) return launch_bn<false, true, true, EPI_STORE, __nv_bfloat16>(p, s);
-    return launch_bn<false, false, true, EPI_STORE, __nv_bfloat16>(p, s);
+    if (p.epi == EPI_GLU) return launch_bn<false, false, EPI_GLU, B>(&p, 1, s);
+    return launch_bn<false, false, EPI_GLU_BWD, B>(&p, 1, s);
+}
+
+cudaError_t launch_gradients_tc(const Product *dx, const Product *dw, cudaStream_t s) {
+    Product p[2];
+    int n = 0;
+    if (dw) p[n++] = *dw;
+    if (dx) p[n++] = *dx;
+    if (n == 2 && (p[0].K + 63) / 64 < (p[1].K + 63) / 64 * p[1].nseg) std::swap(p[0], p[1]);   // longer tiles first
+    return launch_bn<false, true, EPI_STORE, __nv_bfloat16>(p, n, s);
 }
 
 }  // namespace dense

@@ -121,20 +121,52 @@ __device__ __forceinline__ void store_32x32(uint8_t *stage, const float v[32], O
         *reinterpret_cast<uint4 *>(stage + slot(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
-    const int c = lane % kPieces;
+    if (vec) {
+        const int c = lane % kPieces;
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 32 / kPieces) {
-        const int r = r0 + lane / kPieces;
-        if (r >= rows || c * kPer >= cols) continue;
-        const uint4 w = *reinterpret_cast<const uint4 *>(stage + slot(r, c));
-        O *d = dst + (long long)r * ld + c * kPer;
-        if (vec && c * kPer + kPer <= cols) *reinterpret_cast<uint4 *>(d) = w;
-        else {
-            const O *e = reinterpret_cast<const O *>(&w);
+        for (int r0 = 0; r0 < 32; r0 += 32 / kPieces) {
+            const int r = r0 + lane / kPieces;
+            if (r >= rows || c * kPer >= cols) continue;
+            const uint4 w = *reinterpret_cast<const uint4 *>(stage + slot(r, c));
+            O *d = dst + (long long)r * ld + c * kPer;
+            if (c * kPer + kPer <= cols) *reinterpret_cast<uint4 *>(d) = w;
+            else {
+                const O *e = reinterpret_cast<const O *>(&w);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (c * kPer + i < cols) d[i] = e[i];
+                for (int i = 0; i < kPer; ++i)
+                    if (c * kPer + i < cols) d[i] = e[i];
+            }
         }
+    } else if (lane < cols) {   // one element a lane, one row at a time
+        for (int r = 0; r < min(rows, 32); ++r)
+            dst[(long long)r * ld + lane] = *reinterpret_cast<const O *>(stage + slot(r, lane / kPer) + lane % kPer * sizeof(O));
+    }
+}
+// The reverse for bf16: 32 x 32 elements at src, this lane's row into v (zeros outside).
+__device__ __forceinline__ void load_32x32(uint8_t *stage, float v[32], const __nv_bfloat16 *src, long long ld, int rows,
+                                           int cols, bool vec) {
+    const int lane = threadIdx.x & 31;
+    uint4 w[4];
+    if (vec && cols == 32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            w[c] = lane < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (long long)lane * ld) + c) : make_uint4(0, 0, 0, 0);
+    } else {
+        auto slot = [&](int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
+        __syncwarp();
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
+            *reinterpret_cast<uint16_t *>(stage + slot(r, lane >> 3) + (lane & 7) * 2) =
+                r < rows && lane < cols ? __ldg(reinterpret_cast<const uint16_t *>(src + (long long)r * ld + lane)) : 0;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4 *>(stage + slot(lane, c));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * c + i] = bf16_bits_to_f32(i & 1 ? u[i >> 1] >> 16 : u[i >> 1] & 0xFFFFu);
     }
 }
 

@@ -240,7 +240,9 @@ def _call(run, query, which, args, layout, workspace, dev, s, name):
 
 def quant_i8(x, q=None, scale=None, stream=None):
     """moeq_quant_i8: rows of x (float32 or bfloat16 [M][K], unit column
-    stride) to (q int8 [M][K], scale float32 [M]), x ~ q * scale[:, None]."""
+    stride) to (q int8 [M][K], scale float32 [M]), x ~ q * scale[:, None].  A
+    q made here starts its rows on multiples of 16 bytes (a view of a wider
+    buffer where K is not one), as the products take it without a copy."""
     import torch
     dev, s = _enter(x, stream, "quant_i8")
     if s is None:
@@ -250,8 +252,10 @@ def quant_i8(x, q=None, scale=None, stream=None):
         _bad("quant_i8: x is not 2-D")
     M, K = x.shape
     if q is None:
-        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
-        ldq = K
+        ldq = (K + 15) // 16 * 16
+        q = torch.empty((M, ldq), dtype=torch.int8, device=x.device)
+        if ldq != K:
+            q = q[:, :K]
     else:
         ldq = _ld(q, M, K, torch.int8, dev, "quant_i8: q")
     if scale is None:
