@@ -119,8 +119,8 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, int cluste
 }
 
 // ---- launchers ----
-// f32, any strides and alignment (dense_simt.cu)
-cudaError_t launch_product_simt(const Product &p, cudaStream_t s);
+// f32, any strides and alignment (dense_f32.cu)
+cudaError_t launch_product_f32(const Product &p, cudaStream_t s);
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
 // dx and dW (both weights') in one launch, either of them NULL; bf16, operands

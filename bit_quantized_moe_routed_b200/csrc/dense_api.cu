@@ -98,7 +98,7 @@ struct Packing {
     cudaError_t run(cudaStream_t s) const { return n ? launch_pack(c, n, es, s) : cudaSuccess; }
 };
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
-    if (p.in_dtype == MOEQ_ACT_F32) return launch_product_simt(p, s);
+    if (p.in_dtype == MOEQ_ACT_F32) return launch_product_f32(p, s);
     if (stream_supported(p)) return launch_product_stream(p, s);
     return skinny_supported(p) ? launch_product_skinny(p, s) : launch_product_tc(p, s);
 }
@@ -107,8 +107,8 @@ cudaError_t launch_gradients(const Product *dx, const Product *dw, cudaStream_t 
     const Product *any = dx ? dx : dw;
     cudaError_t e = cudaSuccess;
     if (any->in_dtype == MOEQ_ACT_F32) {
-        if (dx) e = launch_product_simt(*dx, s);
-        if (dw && e == cudaSuccess) e = launch_product_simt(*dw, s);
+        if (dx) e = launch_product_f32(*dx, s);
+        if (dw && e == cudaSuccess) e = launch_product_f32(*dw, s);
         return e;
     }
     if (dx && skinny_supported(*dx)) {
