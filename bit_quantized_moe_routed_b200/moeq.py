@@ -220,7 +220,7 @@ def _vec(t, n, dev, what):
     return t.data_ptr()
 
 
-def _call(run, query, which, args, layout, workspace, dev, s, name):
+def _call(run, query, which, args, layout, workspace, t, s, name):
     """One call; ``args`` lacks the workspace's address and size.  Without a
     workspace the call is tried as it is (a call that lacks one is refused
     before any work); where one is needed it is allocated on the call's
@@ -233,9 +233,9 @@ def _call(run, query, which, args, layout, workspace, dev, s, name):
         if n <= 0:
             raise MoeqError(code, name)
         import torch
-        workspace = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        _bad(f"{name}: workspace is not contiguous on cuda:{dev}")
+        workspace = torch.empty(n, dtype=torch.uint8, device=t.device)
+    elif workspace.get_device() != t.get_device() or not workspace.is_contiguous():
+        _bad(f"{name}: workspace is not contiguous on {t.device}")
     _check(run(layout.pack(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size()), s), name)
 
 
@@ -289,7 +289,7 @@ def _i8(name, run, n_w, xq, xs, w0, s0, w1, s1, out, dtype, workspace, dev, s):
         a1, ld1, p1 = w1.data_ptr(), _ld(w1, N, K, i8, dev, name), _vec(s1, N, dev, name)
     _call(run, _lib.moeq_i8_workspace, n_w,
           (T, K, N, act, xq.data_ptr(), ldx, px, w0.data_ptr(), a1, ld0, ld1, p0, p1, out.data_ptr(), ldo), I8_ARGS,
-          workspace, dev, s, name)
+          workspace, xq, s, name)
     return out
 
 
@@ -347,7 +347,7 @@ def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, stream=N
     else:
         ldh = _ld(out, T, N, dt, dev, "glu: out")
     _call(_lib.moeq_glu, _lib.moeq_glu_workspace, 0, head + (out.data_ptr(), ldh, 0, 0, 0, 0, 0, 0, 0, 0), GLU_ARGS,
-          workspace, dev, s, "glu")
+          workspace, x, s, "glu")
     return out if gu is None else (out, gu)
 
 
@@ -386,7 +386,7 @@ def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None
         if n < 0:
             _bad(what)
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _call(_lib.moeq_glu_backward, _lib.moeq_glu_workspace, 1, args, GLU_ARGS, workspace, dev, s, what)
+    _call(_lib.moeq_glu_backward, _lib.moeq_glu_workspace, 1, args, GLU_ARGS, workspace, x, s, what)
     return dx, dw_gate, dw_up
 
 
