@@ -14,8 +14,8 @@ cudaError_t launch_quant_i8(const void *x, int dtype, int rows, int cols, long l
 namespace dense {
 namespace {
 
-constexpr long long kMaxDim = 1LL << 21;      // hidden, inter, n_in, n_out
-constexpr int kMaxTokens = 1 << 30;
+constexpr long long kMaxDim = 1LL << 20;      // hidden, inter, n_out
+constexpr int kMaxTokens = 1 << 30;           // and columns of moeq_quant_i8
 constexpr long long kMaxLd = 1LL << 36;
 constexpr int kMaxI8K = 131071;               // 2^14 K < 2^31
 
@@ -223,7 +223,7 @@ using namespace moeq::dense;
 
 extern "C" moeq_status moeq_quant_i8(const void *x, int32_t dtype, int32_t n_rows, int32_t n_cols, int64_t ldx,
                                      int8_t *q, int64_t ldq, float *scale, void *stream) {
-    if (!known_dtype(dtype) || n_rows < 0 || n_cols < 1) return MOEQ_ERR_INVALID_ARGUMENT;
+    if (!known_dtype(dtype) || n_rows < 0 || n_cols < 1 || n_cols > kMaxTokens) return MOEQ_ERR_INVALID_ARGUMENT;
     if (n_rows == 0) return MOEQ_OK;
     const int es = elem_size(dtype);
     if (!matrix_ok(x, n_cols, ldx, es) || !matrix_ok(q, n_cols, ldq, 1) || !scale || ((uintptr_t)scale & 3u))

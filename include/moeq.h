@@ -365,7 +365,8 @@ MOEQ_API moeq_status moeq_vq_encode(const float *w, int32_t n_rows, int32_t n_co
  * scale = 0; a row that holds a NaN or an infinity gets q = 0, scale = NaN,
  * which makes its products NaN.  Serves activations (a row is a token) and
  * weights (a row is an output channel).
- *   x      device, dtype (moeq_dtype), [n_rows][n_cols], row stride ldx
+ *   x      device, dtype (moeq_dtype), [n_rows][n_cols], row stride ldx;
+ *          n_cols 1..2^30
  *   q      device int8 [n_rows][n_cols], row stride ldq; overwritten
  *   scale  device f32 [n_rows]; overwritten
  * n_rows == 0 is a no-op.  Errors: INVALID_ARGUMENT (NULL, sizes, strides,
@@ -377,7 +378,7 @@ MOEQ_API moeq_status moeq_quant_i8(const void *x, int32_t dtype, int32_t n_rows,
 typedef struct {
     int32_t n_tokens;         /* T, 0 (a no-op) to 2^30                         */
     int32_t n_in;             /* K, 1..131071 (a sum of K products fits int32)  */
-    int32_t n_out;            /* N, 1..2^21                                     */
+    int32_t n_out;            /* N, 1..2^20                                     */
     int32_t out_dtype;        /* moeq_dtype of out                              */
     const int8_t *x;          /* device [T][K], row stride ldx                  */
     int64_t ldx;
@@ -413,8 +414,8 @@ MOEQ_API int64_t moeq_i8_workspace(const moeq_i8_args *a, int32_t n_w);
  * description names. */
 typedef struct {
     int32_t n_tokens;         /* T, 0..2^30                                     */
-    int32_t hidden;           /* H, 1..2^21                                     */
-    int32_t inter;            /* I, 1..2^21                                     */
+    int32_t hidden;           /* H, 1..2^20                                     */
+    int32_t inter;            /* I, 1..2^20                                     */
     int32_t dtype;            /* moeq_dtype of every array                      */
     const void *x;            /* device [T][H], row stride ldx                  */
     int64_t ldx;
@@ -437,7 +438,10 @@ typedef struct {
 /* h[t] = silu(W_gate x[t]) * (W_up x[t]): both projections (f32 sums), the
  * activation and the product in one pass, rounded once to dtype.  With gu,
  * the two projections are also written, rounded to dtype, for a backward
- * pass.  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.  Errors:
+ * pass.  f32 operands are multiplied in parts of 11 significand bits (three
+ * products of parts, off by at most 2^-19 of a product's magnitude in sum and
+ * about 2^-24 on average); an infinity among them may come out as NaN, and
+ * parts below 2^-126 may count as zero.  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.  Errors:
  * INVALID_ARGUMENT (NULL, sizes, strides, unknown dtype, misaligned elements,
  * overlap, a workspace that is too small or misaligned), CUDA. */
 MOEQ_API moeq_status moeq_glu(const moeq_glu_args *a, void *stream);

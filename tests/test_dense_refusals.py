@@ -61,7 +61,7 @@ QUANT = dict(x=ADDR["x"], dt=1, M=4, K=64, ldx=64, q=ADDR["out"], ldq=64, sc=ADD
 
 @pytest.mark.parametrize("bad", [
     dict(x=None), dict(q=None), dict(sc=None), dict(dt=2), dict(dt=-1), dict(M=-1), dict(K=0), dict(ldx=63),
-    dict(ldq=63), dict(x=ADDR["x"] + 1), dict(dt=0, x=ADDR["x"] + 2), dict(sc=ADDR["s0"] + 2), dict(ldx=1 << 40),
+    dict(ldq=63), dict(K=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 31), dict(x=ADDR["x"] + 1), dict(dt=0, x=ADDR["x"] + 2), dict(sc=ADDR["s0"] + 2), dict(ldx=1 << 40),
     dict(q=ADDR["x"]), dict(q=ADDR["x"] + 3 * 128 + 127), dict(sc=ADDR["x"] + 64), dict(sc=ADDR["out"]),
 ])
 def test_quant_i8_refuses(moeq, bad):
@@ -79,7 +79,7 @@ def test_no_tokens_is_a_no_op(moeq):
 
 
 I8_BAD = [
-    dict(T=-1), dict(K=0), dict(K=131072, ldx=131072, ld0=131072, ld1=131072), dict(N=0), dict(N=(1 << 21) + 1),
+    dict(T=-1), dict(K=0), dict(K=131072, ldx=131072, ld0=131072, ld1=131072), dict(N=0), dict(N=(1 << 20) + 1),
     dict(dt=3), dict(x=0), dict(sx=0), dict(w0=0), dict(s0=0), dict(out=0), dict(ldx=63), dict(ld0=63), dict(ldo=31),
     dict(out=ADDR["out"] + 1), dict(dt=0, out=ADDR["out"] + 2), dict(sx=ADDR["sx"] + 1), dict(s0=ADDR["s0"] + 2),
     dict(out=ADDR["x"]), dict(out=ADDR["w0"] + 100), dict(out=ADDR["sx"]), dict(out=ADDR["s0"] + 64),
@@ -108,7 +108,7 @@ def test_int8_products_refuse_the_wrong_number_of_weights(moeq):
 
 
 GLU_BAD = [
-    dict(T=-1), dict(H=0), dict(I=0), dict(H=(1 << 21) + 1, ldx=1 << 22, ld0=1 << 22, ld1=1 << 22, lddx=1 << 22), dict(dt=2),
+    dict(T=-1), dict(H=0), dict(I=0), dict(H=(1 << 20) + 1, ldx=1 << 22, ld0=1 << 22, ld1=1 << 22, lddx=1 << 22), dict(dt=2),
     dict(x=0), dict(w0=0), dict(w1=0), dict(ldx=63), dict(ld0=63), dict(ld1=63), dict(x=ADDR["x"] + 1),
     dict(dt=0, w1=ADDR["w1"] + 2), dict(gu=ADDR["gu"] + 1),
 ]

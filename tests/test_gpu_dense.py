@@ -496,3 +496,112 @@ def test_the_binding_refuses(moeq):
         with pytest.raises(moeq.MoeqError):
             call()
             raise AssertionError(f"call {k} was taken")
+
+
+# --------------------------------------------------- what the kernels' rules rest on
+def test_quant_i8_every_pair_of_bf16_significands(moeq):
+    """bf16 quotients: every significand of x against every one of the row's
+    largest, ten binades down: exact halves among them go to the even integer."""
+    torch = torch_mod()
+    m = torch.arange(128, 256, dtype=torch.float64)
+    top = m[:, None]
+    x = torch.cat([m * 2.0 ** -j for j in range(11)])[None].expand(128, -1)
+    x = torch.where(x <= top, x, torch.zeros_like(x))
+    rows = torch.cat([x, -x, top], dim=1).to(torch.bfloat16).cuda()
+    q, s = moeq.quant_i8(rows)
+    rq, rs = quant_ref(rows)
+    assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+    t = rows.double().cpu().numpy() * 127 / rows.double().abs().amax(1, keepdim=True).cpu().numpy()
+    # halves did occur: for a = 254 alone t = x / 2, a half for the 63 odd x below it and their negatives
+    assert (np.abs(t - np.trunc(t)) == 0.5).sum() >= 126
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 16, 17, 100, 256, 257, 1000])
+def test_tokens_do_not_see_each_other(moeq, T):
+    """A NaN or an infinity in one token's row stays in that token's results."""
+    torch = torch_mod()
+    H, I = 200, 136
+    for dtype in ("bf16", "f32"):
+        x, wg, wu = mat(T, H, dtype, 1), mat(I, H, dtype, 2, scale=0.1), mat(I, H, dtype, 3, scale=0.1)
+        want = moeq.glu(x, wg, wu)
+        y = x.clone()
+        y[T // 2, 7] = float("nan")
+        y[0, 0] = float("inf") if T > 1 else float("nan")
+        got = moeq.glu(y, wg, wu)
+        rows = [r for r in range(T) if r not in (0, T // 2)]
+        assert torch.equal(got[rows], want[rows])
+        assert torch.isnan(got[T // 2]).all()
+        # nor does a weight row's
+        w2 = wg.clone()
+        w2[5, 3] = float("nan")
+        got = moeq.glu(x, w2, wu)
+        cols = [c for c in range(I) if c != 5]
+        assert torch.equal(got[:, cols], want[:, cols]) and torch.isnan(got[:, 5]).all()
+
+
+def test_f32_parts_keep_their_exactness(moeq):
+    """f32 operands with up to 11 significand bits are single parts: products
+    and short sums of them are exact, whatever the sizes and alignment."""
+    torch = torch_mod()
+    for T, H, I in ((3, 32, 40), (70, 31, 65), (300, 32, 100)):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(T)
+        x = torch.randint(-31, 32, (T, H), generator=g, device="cuda").float()
+        wg, wu = (torch.randint(-31, 32, (I, H), generator=g, device="cuda").float() for _ in range(2))
+        _, gu = moeq.glu(x, wg, wu, save=True)      # |sums| <= 32 * 961 < 2^24
+        assert torch.equal(gu[0].double(), x.double() @ wg.double().t())
+        assert torch.equal(gu[1].double(), x.double() @ wu.double().t())
+
+
+def test_wide_rows_far_apart(moeq):
+    """Offsets beyond 2^31 elements: a few rows of a buffer with a huge row stride."""
+    torch = torch_mod()
+    ld = (1 << 30) + 64
+    buf = torch.empty(3 * ld, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((3, 64), (ld, 1))
+    h = buf.as_strided((3, 48), (ld, 1), 4096)
+    src = mat(3, 64, "bf16", 1)
+    x.copy_(src)
+    wg, wu = mat(48, 64, "bf16", 2, scale=0.2), mat(48, 64, "bf16", 3, scale=0.2)
+    want = moeq.glu(src, wg, wu)
+    moeq.glu(x, wg, wu, out=h)
+    assert torch.equal(h, want)
+    # the same rows as the dense kernels' weights (20 tokens: tensor maps with this stride)
+    y = mat(20, 64, "bf16", 4)
+    for t in (y, y[:2]):
+        a, b = moeq.glu(t, src, src), moeq.glu(t, x, x)
+        assert torch.equal(a, b)
+    q, s = moeq.quant_i8(x)
+    assert np.array_equal(q.cpu().numpy(), quant_ref(src)[0])
+    del buf
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of the dense operators are captured ones."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from bit_quantized_moe_routed_b200 import moeq
+g = torch.Generator(device="cuda"); g.manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+sets = [(r(T, 136), r(72, 136) * 0.1, r(72, 136) * 0.1, r(T, 72)) for T in (2, 40, 300)]
+def step(x, a, b, d):
+    h, gu = moeq.glu(x, a, b, save=True)
+    q, s = moeq.quant_i8(x)
+    qa, sa = moeq.quant_i8(a)
+    return (h, gu) + tuple(moeq.glu_backward(d, x, a, b, gu=gu)) + (moeq.matmul_i8(q, s, qa, sa), moeq.glu(x.float(), a.float(), b.float()))
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    got = [step(*s) for s in sets]
+graph.replay()
+torch.cuda.synchronize()
+for s, o in zip(sets, got):
+    assert all(torch.equal(p, q) for p, q in zip(step(*s), o))
+print("captured ok")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
