@@ -3,7 +3,9 @@
 ``python -m bit_quantized_moe_routed_b200.build [--force] [-v]``.  Each
 ``csrc/*.cu`` compiles to ``_build/<name>.o`` (in parallel, skipped when up
 to date), then they link into ``bit_quantized_moe_routed_b200/libmoeq.so``.
-No GPU is needed: nvcc cross-compiles.
+No GPU is needed: nvcc cross-compiles.  ``csrc/torch_calls.cpp`` (the torch
+side of the dense operators' Python calls) compiles with g++ against the
+installed torch into ``_torch_calls.so`` beside it.
 """
 from __future__ import annotations
 
@@ -21,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 SO = os.path.join(PKG, "libmoeq.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_SO = os.path.join(PKG, "_torch_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -48,6 +52,33 @@ def _compile(src: str, force: bool, verbose: bool, extra: list) -> str:
     return obj
 
 
+def _build_calls(force: bool, verbose: bool) -> None:
+    deps = (CALLS_SRC, os.path.join(INCLUDE, "moeq.h"))
+    if (not force and os.path.exists(CALLS_SO)
+            and os.path.getmtime(CALLS_SO) >= max(os.path.getmtime(f) for f in deps)):
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = CALLS_SO + f".tmp{os.getpid()}"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DUSE_CUDA",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        cmd += ["-isystem" if d != INCLUDE else "-I", d]
+    cmd += [CALLS_SRC, "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+            "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_SO)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -62,6 +93,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, SO)
+    _build_calls(force, verbose)
     return SO
 
 

@@ -1,4 +1,5 @@
-"""Python binding of libmoeq (ctypes; argument marshalling only).
+"""Python binding of libmoeq (ctypes; argument marshalling only, compiled for
+the dense operators, whose calls are short).
 
 Every step of the layer runs in the CUDA library; this module only turns
 torch tensors / numpy arrays into pointers, sizes and the current CUDA
@@ -8,7 +9,6 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 import struct
 
@@ -82,7 +82,7 @@ for _f in ("moeq_layer_create", "moeq_upload_weights", "moeq_forward", "moeq_for
 
 
 # the argument structs of the dense operators, packed as the C compiler lays
-# them out (native sizes and alignment)
+# them out (native sizes and alignment), for direct calls of the C ABI
 I8_ARGS = struct.Struct("@4i Pq P 2P 2q 2P Pq Pq")      # moeq_i8_args
 GLU_ARGS = struct.Struct("@4i Pq 2P 2q P Pq Pq Pq 2P 2q Pq")   # moeq_glu_args
 _lib.moeq_quant_i8.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_void_p, C.c_int64,
@@ -158,85 +158,38 @@ def vq_encode(w, book13, book8=None, gain=None, col_weight=None, stream=None):
     return idx13, idx8
 
 
-# The dense operators are called once a layer and step, some of them for a
-# few microseconds of device work: their wrappers build messages only when
-# they raise, ask for the workspace's size only when one is needed, and give
-# torch's allocations their sizes one by one (half the time of a tuple).
-def _bad(what):
-    raise MoeqError(INVALID_ARGUMENT, what)
+class _TorchCalls:
+    """The compiled calls of the dense operators (``_torch_calls.so``: tensor
+    checks, allocation, the C call), loaded on first use; refusals come back
+    as MoeqError."""
+
+    def __getattr__(self, name):
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries before the module that needs them)
+        global _calls
+        path = os.path.join(_HERE, "_torch_calls.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m bit_quantized_moe_routed_b200.build`")
+        spec = importlib.util.spec_from_file_location("_torch_calls", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(_check, *(C.cast(getattr(_lib, f), C.c_void_p).value for f in (
+            "moeq_quant_i8", "moeq_matmul_i8", "moeq_glu_i8", "moeq_i8_workspace", "moeq_glu", "moeq_glu_backward",
+            "moeq_glu_workspace")))
+        _calls = mod
+        return getattr(mod, name)
 
 
-def _enter(t, stream, name):
-    """(device index, raw stream) of a call on the current stream of t's
-    device, which is the current device; or (device index, None): the call is
-    to be made again inside _on(t, stream)."""
+_calls = _TorchCalls()
+
+
+def _on(t, stream, name):
+    """Context of a dense call on ``stream``: what it allocates belongs to that stream."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        _bad(f"{name}: a cuda tensor is needed")
-    dev = t.get_device()
-    if stream is not None:
-        if stream.device_index != dev:
-            _bad(f"{name}: stream on {stream.device}, tensor on {t.device}")
-        return dev, None
-    if torch._C._cuda_getDevice() != dev:
-        return dev, None
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _on(dev, stream):
-    """Context of a call on ``stream`` (or the current stream of device
-    ``dev``): allocations made in it belong to that stream."""
-    import torch
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev)
-
-
-def _act(t, what):
-    """moeq_dtype of a tensor."""
-    import torch
-    if t.dtype is torch.bfloat16:
-        return 1
-    if t.dtype is not torch.float32:
-        _bad(f"{what}: dtype {t.dtype}")
-    return 0
-
-
-def _ld(t, rows, cols, dtype, dev, what):
-    """Row stride of a 2-D cuda tensor with unit column stride, checked
-    against the shape, dtype and device it must have."""
-    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
-        _bad(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, need {dtype} {(rows, cols)} on cuda:{dev}")
-    if t.is_contiguous():
-        return cols
-    rs, cs = t.stride()
-    if cs != 1 and cols > 1:
-        _bad(f"{what}: column stride {cs}")
-    return rs if rows > 1 else max(rs, cols)
-
-
-def _vec(t, n, dev, what):
-    import torch
-    if t.dtype is not torch.float32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
-        _bad(f"{what}: need contiguous float32 ({n},) on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _call(run, query, which, args, layout, workspace, t, s, name):
-    """One call; ``args`` lacks the workspace's address and size.  Without a
-    workspace the call is tried as it is (a call that lacks one is refused
-    before any work); where one is needed it is allocated on the call's
-    stream."""
-    if workspace is None:
-        code = run(layout.pack(*args, 0, 0), s)
-        if code == OK:
-            return
-        n = query(layout.pack(*args, 0, 0), which) if code == INVALID_ARGUMENT else 0
-        if n <= 0:
-            raise MoeqError(code, name)
-        import torch
-        workspace = torch.empty(n, dtype=torch.uint8, device=t.device)
-    elif workspace.get_device() != t.get_device() or not workspace.is_contiguous():
-        _bad(f"{name}: workspace is not contiguous on {t.device}")
-    _check(run(layout.pack(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size()), s), name)
+    if not isinstance(t, torch.Tensor) or stream.device != t.device:
+        raise MoeqError(INVALID_ARGUMENT, f"{name}: stream on {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 def quant_i8(x, q=None, scale=None, stream=None):
@@ -244,90 +197,37 @@ def quant_i8(x, q=None, scale=None, stream=None):
     stride) to (q int8 [M][K], scale float32 [M]), x ~ q * scale[:, None].  A
     q made here starts its rows on multiples of 16 bytes (a view of a wider
     buffer where K is not one), as the products take it without a copy."""
-    import torch
-    dev, s = _enter(x, stream, "quant_i8")
-    if s is None:
-        with _on(dev, stream):
-            return quant_i8(x, q, scale)
-    if x.dim() != 2:
-        _bad("quant_i8: x is not 2-D")
-    M, K = x.shape
-    if q is None:
-        ldq = (K + 15) // 16 * 16
-        q = torch.empty(M, ldq, dtype=torch.int8, device=x.device)
-        if ldq != K:
-            q = q.as_strided((M, K), (ldq, 1))
-    else:
-        ldq = _ld(q, M, K, torch.int8, dev, "quant_i8: q")
-    if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    code = _lib.moeq_quant_i8(x.data_ptr(), _act(x, "quant_i8: x"), M, K, _ld(x, M, K, x.dtype, dev, "quant_i8: x"),
-                              q.data_ptr(), ldq, _vec(scale, M, dev, "quant_i8: scale"), s)
-    if code:
-        _check(code, "moeq_quant_i8")
-    return q, scale
+    if stream is not None:
+        with _on(x, stream, "quant_i8"):
+            return _calls.quant_i8(x, q, scale)
+    return _calls.quant_i8(x, q, scale)
 
 
-def _i8(name, run, n_w, xq, xs, w0, s0, w1, s1, out, dtype, workspace, dev, s):
-    import torch
-    if xq.dim() != 2 or w0.dim() != 2:
-        _bad(f"{name}: operands are not 2-D")
-    T, K = xq.shape
-    N = w0.shape[0]
-    i8 = torch.int8
-    if out is None:
-        if dtype not in ACT:
-            _bad(f"{name}: dtype {dtype!r}")
-        act, ldo = ACT[dtype], N
-        out = torch.empty(T, N, dtype=torch.bfloat16 if act else torch.float32, device=xq.device)
-    else:
-        act, ldo = _act(out, name), _ld(out, T, N, out.dtype, dev, name)
-    ldx, px = _ld(xq, T, K, i8, dev, name), _vec(xs, T, dev, name)
-    ld0, p0 = _ld(w0, N, K, i8, dev, name), _vec(s0, N, dev, name)
-    a1 = ld1 = p1 = 0
-    if w1 is not None:
-        a1, ld1, p1 = w1.data_ptr(), _ld(w1, N, K, i8, dev, name), _vec(s1, N, dev, name)
-    _call(run, _lib.moeq_i8_workspace, n_w,
-          (T, K, N, act, xq.data_ptr(), ldx, px, w0.data_ptr(), a1, ld0, ld1, p0, p1, out.data_ptr(), ldo), I8_ARGS,
-          workspace, xq, s, name)
-    return out
+def _out_act(dtype, name):
+    if dtype not in ACT:
+        raise MoeqError(INVALID_ARGUMENT, f"{name}: dtype {dtype!r}")
+    return ACT[dtype]
 
 
 def matmul_i8(xq, xs, wq, ws, out=None, dtype="bf16", workspace=None, stream=None):
     """moeq_matmul_i8: (xq wq^T) xs[:, None] ws with xq int8 [T][K], wq int8
     [N][K], xs float32 [T], ws float32 [N]; [T][N] in ``dtype`` ("bf16" or
     "f32"), or into ``out``."""
-    dev, s = _enter(xq, stream, "matmul_i8")
-    if s is None:
-        with _on(dev, stream):
-            return matmul_i8(xq, xs, wq, ws, out, dtype, workspace)
-    return _i8("matmul_i8", _lib.moeq_matmul_i8, 1, xq, xs, wq, ws, None, None, out, dtype, workspace, dev, s)
+    act = _out_act(dtype, "matmul_i8")
+    if stream is not None:
+        with _on(xq, stream, "matmul_i8"):
+            return _calls.matmul_i8(xq, xs, wq, ws, out, act, workspace)
+    return _calls.matmul_i8(xq, xs, wq, ws, out, act, workspace)
 
 
 def glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out=None, dtype="bf16", workspace=None, stream=None):
     """moeq_glu_i8: silu(G) * U with G, U the products of xq with the int8
     weights [N][K] of both projections, as matmul_i8."""
-    dev, s = _enter(xq, stream, "glu_i8")
-    if s is None:
-        with _on(dev, stream):
-            return glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out, dtype, workspace)
-    return _i8("glu_i8", _lib.moeq_glu_i8, 2, xq, xs, w_gate, s_gate, w_up, s_up, out, dtype, workspace, dev, s)
-
-
-def _glu_common(x, w_gate, w_up, gu, dev, what):
-    if x.dim() != 2 or w_gate.dim() != 2:
-        _bad(f"{what}: operands are not 2-D")
-    T, H = x.shape
-    N = w_gate.shape[0]
-    dt = x.dtype
-    act = _act(x, what)
-    pgu = 0
-    if gu is not None:
-        if gu.dtype is not dt or gu.shape != (2, T, N) or gu.get_device() != dev or not gu.is_contiguous():
-            _bad(f"{what}: gu is not a contiguous {dt} {(2, T, N)} on cuda:{dev}")
-        pgu = gu.data_ptr()
-    return T, H, N, dt, (T, H, N, act, x.data_ptr(), _ld(x, T, H, dt, dev, what), w_gate.data_ptr(), w_up.data_ptr(),
-                         _ld(w_gate, N, H, dt, dev, what), _ld(w_up, N, H, dt, dev, what), pgu)
+    act = _out_act(dtype, "glu_i8")
+    if stream is not None:
+        with _on(xq, stream, "glu_i8"):
+            return _calls.glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out, act, workspace)
+    return _calls.glu_i8(xq, xs, w_gate, s_gate, w_up, s_up, out, act, workspace)
 
 
 def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, stream=None):
@@ -335,20 +235,10 @@ def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, stream=N
     weights [N][H] (float32 or bfloat16, unit column stride).  With ``save``
     (or a ``gu`` buffer [2][T][N]) returns (h, gu) with both projections kept
     for glu_backward."""
-    dev, s = _enter(x, stream, "glu")
-    if s is None:
-        with _on(dev, stream):
-            return glu(x, w_gate, w_up, save, out, gu, workspace)
-    if save and gu is None and x.dim() == 2 and w_gate.dim() == 2:
-        gu = x.new_empty(2, x.shape[0], w_gate.shape[0])
-    T, H, N, dt, head = _glu_common(x, w_gate, w_up, gu, dev, "glu")
-    if out is None:
-        out, ldh = x.new_empty(T, N), N
-    else:
-        ldh = _ld(out, T, N, dt, dev, "glu: out")
-    _call(_lib.moeq_glu, _lib.moeq_glu_workspace, 0, head + (out.data_ptr(), ldh, 0, 0, 0, 0, 0, 0, 0, 0), GLU_ARGS,
-          workspace, x, s, "glu")
-    return out if gu is None else (out, gu)
+    if stream is not None:
+        with _on(x, stream, "glu"):
+            return _calls.glu(x, w_gate, w_up, save, out, gu, workspace)
+    return _calls.glu(x, w_gate, w_up, save, out, gu, workspace)
 
 
 def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None, need_dx=True, need_dw=True,
@@ -357,37 +247,10 @@ def glu_backward(dh, x, w_gate, w_up, gu=None, dx=None, dw_gate=None, dw_up=None
     gradient dh [T][N] of glu's result; ``gu`` as kept by glu, or None to
     compute the projections again.  Gradients left out (``need_dx``,
     ``need_dw``) come back as None."""
-    import torch
-    what = "glu_backward"
-    dev, s = _enter(dh, stream, what)
-    if s is None:
-        with _on(dev, stream):
-            return glu_backward(dh, x, w_gate, w_up, gu, dx, dw_gate, dw_up, need_dx, need_dw, workspace)
-    T, H, N, dt, head = _glu_common(x, w_gate, w_up, gu, dev, what)
-    if not (need_dx or dx is None) or not (need_dw or (dw_gate is None and dw_up is None)):
-        _bad(f"{what}: a buffer for a gradient that is left out")
-    if not (need_dx or need_dw):
-        _bad(f"{what}: no gradient asked for")
-    pdx = lddx = pg = pu = ldg = ldu = 0
-    if need_dx:
-        if dx is None:
-            dx = x.new_empty(T, H)
-        pdx, lddx = dx.data_ptr(), _ld(dx, T, H, dt, dev, what)
-    if need_dw:
-        if dw_gate is None:
-            dw_gate = x.new_empty(N, H)
-        if dw_up is None:
-            dw_up = x.new_empty(N, H)
-        pg, pu = dw_gate.data_ptr(), dw_up.data_ptr()
-        ldg, ldu = _ld(dw_gate, N, H, dt, dev, what), _ld(dw_up, N, H, dt, dev, what)
-    args = head + (0, 0, dh.data_ptr(), _ld(dh, T, N, dt, dev, what), pdx, lddx, pg, pu, ldg, ldu)
-    if workspace is None:
-        n = _lib.moeq_glu_workspace(GLU_ARGS.pack(*args, 0, 0), 1)
-        if n < 0:
-            _bad(what)
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _call(_lib.moeq_glu_backward, _lib.moeq_glu_workspace, 1, args, GLU_ARGS, workspace, x, s, what)
-    return dx, dw_gate, dw_up
+    if stream is not None:
+        with _on(dh, stream, "glu_backward"):
+            return _calls.glu_backward(dh, x, w_gate, w_up, gu, dx, dw_gate, dw_up, need_dx, need_dw, workspace)
+    return _calls.glu_backward(dh, x, w_gate, w_up, gu, dx, dw_gate, dw_up, need_dx, need_dw, workspace)
 
 
 def dense_status(clear=False) -> int:
