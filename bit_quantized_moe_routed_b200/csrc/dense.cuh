@@ -144,6 +144,30 @@ struct Copy {
     long long dst_ld, rows, cols;
 };
 cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s);
+// f32 products from bf16 planes (dense_planes.cu), for more than kF32Rows rows.
+// A matrix's planes: bf16 [3][rows][ld], ld a multiple of 64.
+constexpr int kF32Rows = 32;
+struct Planes {
+    const void *p = nullptr;
+    long long rows = 0, cols = 0, ld = 0;
+};
+struct PlanesProduct {   // as Product
+    long long M = 0, N = 0, K = 0;
+    int nseg = 1, nbatch = 1;
+    Planes a[2], b[2];           // a: per segment, or per batch; b: per segment, or gate / up
+    bool a_t = false;            // a stored [K][M]; b is [K][N] but for the gated block
+    void *out[2] = {nullptr, nullptr};
+    long long old[2] = {0, 0};
+    void *keep[2] = {nullptr, nullptr};   // f32 (EPI_GLU), or planes with `kplane` elements between them
+    long long kld = 0, kplane = 0;
+    const float *dh = nullptr;
+    long long dhld = 0;
+    int epi = EPI_STORE;
+};
+cudaError_t launch_product_planes(const PlanesProduct &p, cudaStream_t s);
+cudaError_t launch_split(const Copy *c, int n, cudaStream_t s);   // dst: planes
+cudaError_t launch_dgate_planes(const float *dh, long long dhld, const float *gu, void *dg, void *du, long long ld,
+                                long long M, long long N, cudaStream_t s);
 // SMs of the current device; address of its status word (dense_tc.cu).
 cudaError_t sm_count(int *n);
 cudaError_t status_word(uint32_t **p);

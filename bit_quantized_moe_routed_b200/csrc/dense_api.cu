@@ -71,11 +71,19 @@ struct Packed {
         ld = (cols * es + 127) / 128 * 128 / es;
         bytes = round256((size_t)rows * ld * es);
     }
+    static Packed planes(long long rows, long long cols) {
+        Packed k;
+        k.ld = (cols + 63) / 64 * 64;
+        k.bytes = round256((size_t)3 * rows * k.ld * 2);
+        return k;
+    }
 };
-// The workspace's parts, in the order they lie in it.
+// The workspace's parts, in the order they lie in it.  planes: f32 operands are
+// multiplied as bf16 planes, which x, w and dgu then hold.
 struct Plan {
+    bool planes = false;
     Packed x, w[2];
-    size_t dgu = 0;            // gradients of the projections, [2][T][dgu_ld]
+    size_t dgu = 0;            // gradients of the projections, [2][T][dgu_ld] (or [2] planes of them)
     long long dgu_ld = 0;
     size_t total() const { return x.bytes + w[0].bytes + w[1].bytes + dgu; }
 };
@@ -95,8 +103,33 @@ struct Packing {
         ld = k.ld;
         ws += k.bytes;
     }
-    cudaError_t run(cudaStream_t s) const { return n ? launch_pack(c, n, es, s) : cudaSuccess; }
+    cudaError_t run(cudaStream_t s, bool planes = false) const {
+        return !n ? cudaSuccess : (planes ? launch_split(c, n, s) : launch_pack(c, n, es, s));
+    }
 };
+// The same product of operands that lie as planes
+PlanesProduct of_planes(const Product &p) {
+    PlanesProduct q;
+    q.M = p.M;
+    q.N = p.N;
+    q.K = p.K;
+    q.nseg = p.nseg;
+    q.nbatch = p.nbatch;
+    q.a_t = p.a_t;
+    for (int i = 0; i < 2; ++i) {
+        if (p.a[i]) q.a[i] = Planes{p.a[i], p.a_t ? p.K : p.M, p.a_t ? p.M : p.K, p.ald};
+        if (p.b[i]) q.b[i] = Planes{p.b[i], p.b_t ? p.K : p.N, p.b_t ? p.N : p.K, p.bld[i]};
+        q.out[i] = p.out[i];
+        q.old[i] = p.old[i];
+        q.keep[i] = p.keep[i];
+    }
+    q.kld = p.kld;
+    q.kplane = p.M * p.kld;
+    q.dh = static_cast<const float *>(p.dh);
+    q.dhld = p.dhld;
+    q.epi = p.epi;
+    return q;
+}
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
     if (p.in_dtype == MOEQ_ACT_F32) return launch_product_f32(p, s);
     if (stream_supported(p)) return launch_product_stream(p, s);
@@ -168,9 +201,14 @@ Plan plan_glu(const moeq_glu_args *a, bool backward) {
         if (!backward || !a->gu || a->dx)
             for (int i = 0; i < 2; ++i) p.w[i] = Packed(a->w[i], a->inter, a->hidden, a->ldw[i], 2);
     }
+    p.planes = a->dtype == MOEQ_ACT_F32 && a->n_tokens > kF32Rows;
+    if (p.planes) {
+        if (!backward || !a->gu || a->dw[0]) p.x = Packed::planes(a->n_tokens, a->hidden);
+        if (!backward || !a->gu || a->dx) p.w[0] = p.w[1] = Packed::planes(a->inter, a->hidden);
+    }
     if (!backward) return p;
     p.dgu_ld = (a->inter + 63) / 64 * 64;
-    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * elem_size(a->dtype));
+    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * (p.planes ? 6 : elem_size(a->dtype)));
     return p;
 }
 
@@ -279,8 +317,12 @@ extern "C" moeq_status moeq_glu(const moeq_glu_args *a, void *stream) {
     Packing pk(a->workspace, es);
     pk.add(plan.x, p.a[0], p.ald, T, H);
     for (int i = 0; i < 2; ++i) pk.add(plan.w[i], p.b[i], p.bld[i], I, H);
-    const cudaError_t e = pk.run(s);
-    return done(e == cudaSuccess ? launch_product(p, s) : e);
+    const cudaError_t e = pk.run(s, plan.planes);
+    if (e != cudaSuccess) return MOEQ_ERR_CUDA;
+    if (plan.planes) {
+        return done(launch_product_planes(of_planes(p), s));
+    }
+    return done(launch_product(p, s));
 }
 
 extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
@@ -309,10 +351,13 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
     Packing pk(a->workspace, es);
     pk.add(plan.x, x, ldx, T, H);
     for (int i = 0; i < 2; ++i) pk.add(plan.w[i], w[i], ldw[i], I, H);
-    cudaError_t e = pk.run(s);
+    cudaError_t e = pk.run(s, plan.planes);
     if (e != cudaSuccess) return MOEQ_ERR_CUDA;
-    char *dg = pk.ws, *du = dg + (size_t)T * plan.dgu_ld * es;
-    if (a->gu) {
+    char *dg = pk.ws, *du = dg + (size_t)T * plan.dgu_ld * (plan.planes ? 6 : es);
+    if (a->gu && plan.planes) {
+        e = launch_dgate_planes(static_cast<const float *>(a->dh), a->lddh, static_cast<const float *>(a->gu), dg, du,
+                                plan.dgu_ld, T, I, s);
+    } else if (a->gu) {
         e = launch_glu_dgate(a->dh, a->lddh, a->gu, dg, du, plan.dgu_ld, T, I, a->dtype, s);
     } else {
         Product p;
@@ -332,7 +377,7 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         p.dhld = a->lddh;
         p.in_dtype = p.out_dtype = a->dtype;
         p.epi = EPI_GLU_BWD;
-        e = launch_product(p, s);
+        e = plan.planes ? launch_product_planes(of_planes(p), s) : launch_product(p, s);
     }
     if (e != cudaSuccess) return MOEQ_ERR_CUDA;
     Product px, pw;
@@ -361,6 +406,11 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         px.bld[i] = ldw[i];
         pw.out[i] = a->dw[i];
         pw.old[i] = a->lddw[i];
+    }
+    if (plan.planes) {
+        if (a->dx) e = launch_product_planes(of_planes(px), s);
+        if (a->dw[0] && e == cudaSuccess) e = launch_product_planes(of_planes(pw), s);
+        return done(e);
     }
     return done(launch_gradients(a->dx ? &px : nullptr, a->dw[0] ? &pw : nullptr, s));
 }

@@ -507,11 +507,12 @@ cudaError_t sm_count(int *n) {
     return e;
 }
 
-cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long long cols, long long ld, int es,
-                     int box_rows) {
-    typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+namespace {
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+cudaError_t encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
+                   const cuuint64_t *strides, const cuuint32_t *box) {
     static std::atomic<EncodeFn> fn{nullptr};
     EncodeFn f = fn.load(std::memory_order_acquire);
     if (!f) {
@@ -523,17 +524,29 @@ cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long lo
         f = reinterpret_cast<EncodeFn>(p);
         fn.store(f, std::memory_order_release);
     }
-    // a single row has no stride of its own
-    const long long pitch = rows > 1 ? ld * es : (cols * es + 15) / 16 * 16;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows};
-    const cuuint32_t es1[2] = {1, 1};
-    const CUresult r = f(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                         const_cast<void *>(base), dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = f(map, type, rank, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long long cols, long long ld, int es,
+                     int box_rows) {
+    // a single row has no stride of its own
+    const long long pitch = rows > 1 ? ld * es : (cols * es + 15) / 16 * 16;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows};
+    return encode(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+                  box);
+}
+
+cudaError_t make_planes_map(CUtensorMap *map, const Planes &m, int box_rows, int box_planes) {
+    const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, 3};
+    const cuuint64_t strides[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.rows * m.ld) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, m.p, dims, strides, box);
 }
 
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s) {

@@ -20,6 +20,9 @@ constexpr long long kWaitCycles = 2000000000LL; // limit of every wait between r
 // The base and the row stride are multiples of 16 bytes.
 cudaError_t make_map(CUtensorMap *map, const void *base, long long rows, long long cols, long long ld, int es,
                      int box_rows);
+// Tensor map over a matrix's planes, 128-byte swizzle, boxes of 64 columns x
+// box_rows x box_planes; reads outside give zeros.
+cudaError_t make_planes_map(CUtensorMap *map, const Planes &m, int box_rows, int box_planes);
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
