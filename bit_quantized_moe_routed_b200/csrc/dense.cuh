@@ -119,8 +119,6 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, int cluste
 }
 
 // ---- launchers ----
-// f32, any strides and alignment (dense_f32.cu)
-cudaError_t launch_product_f32(const Product &p, cudaStream_t s);
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
 // dx and dW (both weights') in one launch, either of them NULL; bf16, operands
@@ -144,9 +142,8 @@ struct Copy {
     long long dst_ld, rows, cols;
 };
 cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s);
-// f32 products from bf16 planes (dense_planes.cu), for more than kF32Rows rows.
-// A matrix's planes: bf16 [3][rows][ld], ld a multiple of 64.
-constexpr int kF32Rows = 32;
+// f32 products from bf16 planes (dense_planes.cu).  A matrix's planes: bf16
+// [3][rows][ld], ld a multiple of 64.
 struct Planes {
     const void *p = nullptr;
     long long rows = 0, cols = 0, ld = 0;
@@ -171,9 +168,9 @@ cudaError_t launch_dgate_planes(const float *dh, long long dhld, const float *gu
 // SMs of the current device; address of its status word (dense_tc.cu).
 cudaError_t sm_count(int *n);
 cudaError_t status_word(uint32_t **p);
-// dgu[0/1] (row stride ld) = the gradients of the kept projections gu [2][M][N]
+// dg, du (row stride ld) = the gradients of the kept projections gu [2][M][N], bf16
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,
-                             long long M, long long N, int dtype, cudaStream_t s);
+                             long long M, long long N, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace moeq

@@ -131,21 +131,13 @@ PlanesProduct of_planes(const Product &p) {
     return q;
 }
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
-    if (p.in_dtype == MOEQ_ACT_F32) return launch_product_f32(p, s);
     if (stream_supported(p)) return launch_product_stream(p, s);
     return skinny_supported(p) ? launch_product_skinny(p, s) : launch_product_tc(p, s);
 }
 
 cudaError_t launch_gradients(const Product *dx, const Product *dw, cudaStream_t s) {
-    const Product *any = dx ? dx : dw;
-    cudaError_t e = cudaSuccess;
-    if (any->in_dtype == MOEQ_ACT_F32) {
-        if (dx) e = launch_product_f32(*dx, s);
-        if (dw && e == cudaSuccess) e = launch_product_f32(*dw, s);
-        return e;
-    }
     if (dx && skinny_supported(*dx)) {
-        e = launch_product_skinny(*dx, s);
+        const cudaError_t e = launch_product_skinny(*dx, s);
         dx = nullptr;
         if (!dw || e != cudaSuccess) return e;
     }
@@ -201,14 +193,14 @@ Plan plan_glu(const moeq_glu_args *a, bool backward) {
         if (!backward || !a->gu || a->dx)
             for (int i = 0; i < 2; ++i) p.w[i] = Packed(a->w[i], a->inter, a->hidden, a->ldw[i], 2);
     }
-    p.planes = a->dtype == MOEQ_ACT_F32 && a->n_tokens > kF32Rows;
+    p.planes = a->dtype == MOEQ_ACT_F32;
     if (p.planes) {
         if (!backward || !a->gu || a->dw[0]) p.x = Packed::planes(a->n_tokens, a->hidden);
         if (!backward || !a->gu || a->dx) p.w[0] = p.w[1] = Packed::planes(a->inter, a->hidden);
     }
     if (!backward) return p;
     p.dgu_ld = (a->inter + 63) / 64 * 64;
-    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * (p.planes ? 6 : elem_size(a->dtype)));
+    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * (p.planes ? 6 : 2));
     return p;
 }
 
@@ -358,7 +350,7 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         e = launch_dgate_planes(static_cast<const float *>(a->dh), a->lddh, static_cast<const float *>(a->gu), dg, du,
                                 plan.dgu_ld, T, I, s);
     } else if (a->gu) {
-        e = launch_glu_dgate(a->dh, a->lddh, a->gu, dg, du, plan.dgu_ld, T, I, a->dtype, s);
+        e = launch_glu_dgate(a->dh, a->lddh, a->gu, dg, du, plan.dgu_ld, T, I, s);
     } else {
         Product p;
         p.M = T;

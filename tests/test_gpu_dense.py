@@ -540,7 +540,7 @@ def test_tokens_do_not_see_each_other(moeq, T):
 
 
 def test_f32_parts_keep_their_exactness(moeq):
-    """f32 operands with up to 11 significand bits are single parts: products
+    """f32 operands with up to 8 significand bits are single parts: products
     and short sums of them are exact, whatever the sizes and alignment."""
     torch = torch_mod()
     for T, H, I in ((3, 32, 40), (70, 31, 65), (300, 32, 100)):
@@ -551,6 +551,20 @@ def test_f32_parts_keep_their_exactness(moeq):
         _, gu = moeq.glu(x, wg, wu, save=True)      # |sums| <= 32 * 961 < 2^24
         assert torch.equal(gu[0].double(), x.double() @ wg.double().t())
         assert torch.equal(gu[1].double(), x.double() @ wu.double().t())
+
+
+def test_f32_values_near_the_ends_of_the_range(moeq):
+    """Finite values whose nearest bf16 is infinite, and small ones, keep their
+    accuracy: scaling an operand by a power of two scales the projections."""
+    torch = torch_mod()
+    for T in (2, 40, 300):
+        x, w = mat(T, 96, "f32", 5), mat(50, 96, "f32", 6, scale=0.2)
+        x = x / x.abs().max()                       # largest 1: times 3.4028e38 it is near the largest f32
+        for sx, sw in ((3.4028e38, 2.0 ** -100), (2.0 ** 60, 2.0 ** -90), (2.0 ** -60, 2.0 ** -40)):
+            y, v = x * sx, w * sw
+            _, gu = moeq.glu(y, v, v, save=True)
+            g, u, eg, eu = projections(y, v, v)
+            check(gu[0], g, eg + (g.abs() + eg) * EPS["f32"] * 1.001, f"g at {sx} {sw}")
 
 
 def test_wide_rows_far_apart(moeq):
