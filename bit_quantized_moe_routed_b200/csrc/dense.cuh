@@ -128,11 +128,12 @@ cudaError_t launch_gradients_tc(const Product *dx, const Product *dw, cudaStream
 constexpr int kStreamRows = 16;
 bool stream_supported(const Product &p);
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
-// bf16 and int8, at most kSkinnyRows rows of A; operands as for
-// launch_product_tc (dense_skinny.cu)
-constexpr int kSkinnyRows = 256;
-bool skinny_supported(const Product &p);
+// bf16 and int8, K split over clusters; operands as for launch_product_tc, no
+// transposed A and no batches (dense_skinny.cu)
 cudaError_t launch_product_skinny(const Product &p, cudaStream_t s);
+// Estimated time of either in ns, without a launch's common 5.5 us (bn: the tile width)
+long long tc_ns(const Product *ps, int n, int sms, int *bn);
+long long skinny_ns(const Product &p, int sms);
 // dst (16-byte aligned base and row stride) = src, rows x cols of es-byte
 // elements, strides in elements; up to three at once.
 struct Copy {

@@ -132,14 +132,24 @@ PlanesProduct of_planes(const Product &p) {
 }
 cudaError_t launch_product(const Product &p, cudaStream_t s) {
     if (stream_supported(p)) return launch_product_stream(p, s);
-    return skinny_supported(p) ? launch_product_skinny(p, s) : launch_product_tc(p, s);
+    int sms = 0, bn = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    return skinny_ns(p, sms) < tc_ns(&p, 1, sms, &bn) ? launch_product_skinny(p, s) : launch_product_tc(p, s);
 }
 
 cudaError_t launch_gradients(const Product *dx, const Product *dw, cudaStream_t s) {
-    if (dx && skinny_supported(*dx)) {
-        const cudaError_t e = launch_product_skinny(*dx, s);
-        dx = nullptr;
-        if (!dw || e != cudaSuccess) return e;
+    // dx by clusters where that saves more than a launch of its own costs; the
+    // choice does not depend on dW, so that asking for less changes no bits
+    if (dx) {
+        int sms = 0, bn = 0;
+        cudaError_t e = sm_count(&sms);
+        if (e != cudaSuccess) return e;
+        if (skinny_ns(*dx, sms) + 3000 < tc_ns(dx, 1, sms, &bn)) {
+            e = launch_product_skinny(*dx, s);
+            dx = nullptr;
+            if (!dw || e != cudaSuccess) return e;
+        }
     }
     return launch_gradients_tc(dx, dw, s);
 }

@@ -444,32 +444,13 @@ cudaError_t launch_t(const Product *ps, int n, int sms, cudaStream_t s) {
     return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), kThreads, R::kSmem, 0, s, a);
 }
 
-// Tile width: 256 columns unless 128 leave the pairs idle less.  A tile of 128
-// columns does half the work of one of 256 in 0.85 of its time when all pairs
-// are busy (measured at 4096 x 4096 x 2048, bf16: 22.6 against 26.5 us a tile;
-// both are fed at 38 to 47 bytes a clock and SM from L2, and the narrow tile
-// needs 1.5 times the bytes per flop), so it pays only when the wide tiles
-// leave more than that share of the pairs without work.
 template <bool I8, bool B_MN, int EPI, typename O>
 cudaError_t launch_bn(const Product *ps, int n, cudaStream_t s) {
-    int sms = 0;
+    int sms = 0, bn = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const long long pairs = sms / 2;
-    long long cost[2];
-    for (int h = 0; h < 2; ++h) {
-        const long long cols = (EPI == EPI_STORE ? 256 : 128) >> h;
-        long long work = 0, longest = 0;      // in K blocks: of all tiles, of the longest round
-        for (int j = 0; j < n; ++j) {
-            const long long t = (ps[j].M + 255) / 256 * ((ps[j].N + cols - 1) / cols) * ps[j].nbatch;
-            const long long kb = (ps[j].K + 63) / 64 * ps[j].nseg;
-            work += t * kb;
-            longest = std::max(longest, (t + pairs - 1) / pairs * kb);
-        }
-        const long long kb1 = (ps[n - 1].K + 63) / 64 * ps[n - 1].nseg;
-        cost[h] = std::max(longest, (work + pairs * kb1 - 1) / (pairs * kb1) * kb1) * (h ? 85 : 100);
-    }
-    return cost[0] <= cost[1] ? launch_t<I8, B_MN, EPI, 256, O>(ps, n, sms, s) : launch_t<I8, B_MN, EPI, 128, O>(ps, n, sms, s);
+    tc_ns(ps, n, sms, &bn);
+    return bn == 256 ? launch_t<I8, B_MN, EPI, 256, O>(ps, n, sms, s) : launch_t<I8, B_MN, EPI, 128, O>(ps, n, sms, s);
 }
 
 __device__ uint32_t g_status;
@@ -547,6 +528,33 @@ cudaError_t make_planes_map(CUtensorMap *map, const Planes &m, int box_rows, int
     const cuuint64_t strides[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.rows * m.ld) * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, m.p, dims, strides, box);
+}
+
+// Measured: a K block of a 256-column tile takes 300 ns with most pairs busy, of
+// a 128-column tile 250 (both are fed at 38 to 47 bytes a clock and SM from L2,
+// and the narrow tile needs 1.5 times the bytes per flop), and a tile no less
+// than its epilogue, 1.5 or 0.8 us.
+long long tc_ns(const Product *ps, int n, int sms, int *bn) {
+    const long long pairs = sms / 2;
+    long long best = 0;
+    for (int h = 0; h < 2; ++h) {
+        const long long cols = (ps[0].epi == EPI_STORE ? 256 : 128) >> h;
+        long long work = 0, longest = 0, least = 0;   // of all tiles; of the rounds of one product; of its last tiles
+        for (int j = 0; j < n; ++j) {
+            const int ke = ps[j].in_dtype == kI8 ? 128 : 64;
+            const long long tiles = (ps[j].M + 255) / 256 * ((ps[j].N + cols - 1) / cols) * ps[j].nbatch;
+            const long long tile = std::max<long long>((ps[j].K + ke - 1) / ke * ps[j].nseg * (h ? 250 : 300), h ? 800 : 1500);
+            work += tiles * tile;
+            longest = std::max(longest, (tiles + pairs - 1) / pairs * tile);
+            least = j ? std::min(least, tile) : tile;
+        }
+        const long long t = std::max(longest, (work + pairs * least - 1) / (pairs * least) * least);
+        if (h == 0 || t < best) {
+            best = t;
+            *bn = h ? 128 : 256;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s) {
