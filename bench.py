@@ -44,7 +44,7 @@ NCU_TRAFFIC = {
                       "bit_quantized_moe_routed_b200/csrc/decode_common.cuh",
                       "bit_quantized_moe_routed_b200/csrc/internal.cuh",
                       "include/moeq.h"),
-                     "2b897f5299762b04da5642c87e146fd68c7baabb52f21d081754eb892716c7f2",
+                     "03c27e330f2b184efdba25b8c17f2e221b9a1c4f40d222a26c0d0ba8fcfe21c5",
                      107049216.0 + 358144.0, "profiles/dec_fused_mx_decode_mxfp4.md"),
 }
 
