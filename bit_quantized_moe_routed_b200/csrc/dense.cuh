@@ -101,10 +101,10 @@ __device__ __forceinline__ void load16_any(const uint8_t *p, int left, bool befo
 // before it touches global memory.  cluster: CTAs of a cluster, 0 for the
 // kernel's own.
 template <typename K, typename... A>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const A &...args) {
+cudaError_t launch_pdl(K kernel, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -118,6 +118,20 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, int cluste
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Blocks of 128 threads for a pass over `rows` rows of `pieces` pieces each:
+// narrow rows share a block.  A thread takes piece blockIdx.x * blockDim.x +
+// threadIdx.x of rows blockIdx.y * blockDim.y + threadIdx.y.
+struct RowGrid {
+    dim3 grid, block;
+    RowGrid(long long rows, long long pieces, int z = 1) {
+        unsigned x = 4;
+        while (x < 128 && x < pieces) x *= 2;
+        block = dim3(x, 128 / x);
+        const long long y = (rows + block.y - 1) / block.y;
+        grid = dim3((unsigned)((pieces + x - 1) / x), (unsigned)(y < 16384 ? y : 16384), (unsigned)z);
+    }
+};
+
 // ---- launchers ----
 // bf16 and int8: A and B with 16-byte aligned bases and row strides (dense_tc.cu)
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
@@ -128,8 +142,8 @@ cudaError_t launch_gradients_tc(const Product *dx, const Product *dw, cudaStream
 constexpr int kStreamRows = 16;
 bool stream_supported(const Product &p);
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
-// bf16 and int8, K split over clusters; operands as for launch_product_tc, no
-// transposed A and no batches (dense_skinny.cu)
+// bf16 and int8, K split over clusters; operands as for launch_product_tc
+// (dense_skinny.cu)
 cudaError_t launch_product_skinny(const Product &p, cudaStream_t s);
 // Estimated time of either in ns, without a launch's common 5.5 us (bn: the tile width)
 long long tc_ns(const Product *ps, int n, int sms, int *bn);

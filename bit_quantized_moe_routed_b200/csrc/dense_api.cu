@@ -139,18 +139,19 @@ cudaError_t launch_product(const Product &p, cudaStream_t s) {
 }
 
 cudaError_t launch_gradients(const Product *dx, const Product *dw, cudaStream_t s) {
-    // dx by clusters where that saves more than a launch of its own costs; the
-    // choice does not depend on dW, so that asking for less changes no bits
-    if (dx) {
-        int sms = 0, bn = 0;
-        cudaError_t e = sm_count(&sms);
+    // one of them by clusters where that saves more than a launch of its own
+    // costs; neither choice depends on the other, so that asking for less changes
+    // no bits
+    int sms = 0, bn = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    for (const Product **p : {&dx, &dw}) {
+        if (!*p || skinny_ns(**p, sms) + 3000 >= tc_ns(*p, 1, sms, &bn)) continue;
+        e = launch_product_skinny(**p, s);
+        *p = nullptr;
         if (e != cudaSuccess) return e;
-        if (skinny_ns(*dx, sms) + 3000 < tc_ns(dx, 1, sms, &bn)) {
-            e = launch_product_skinny(*dx, s);
-            dx = nullptr;
-            if (!dw || e != cudaSuccess) return e;
-        }
     }
+    if (!dx && !dw) return cudaSuccess;
     return launch_gradients_tc(dx, dw, s);
 }
 

@@ -345,12 +345,12 @@ struct SplitArgs {
 // f32 matrices into their planes, four columns a thread (bandwidth bound: 4
 // bytes in, 6 out an element)
 __global__ void __launch_bounds__(128) split_kernel(const __grid_constant__ SplitArgs p) {
-    const int z = blockIdx.z, c = (blockIdx.x * 128 + threadIdx.x) * 4;
+    const int z = blockIdx.z, c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
     pdl_wait_primary();
     pdl_launch_dependents();
     if (c >= p.cols[z]) return;
     const long long plane = p.rows[z] * p.dst_ld[z];
-    for (long long r = blockIdx.y; r < p.rows[z]; r += gridDim.y) {
+    for (long long r = blockIdx.y * blockDim.y + threadIdx.y; r < p.rows[z]; r += gridDim.y * blockDim.y) {
         const float *s = p.src[z] + r * p.ld[z] + c;
         float v[4];
         if (c + 4 <= p.cols[z] && !((uintptr_t)s & 15u)) {
@@ -378,12 +378,12 @@ __global__ void __launch_bounds__(128) dgate_planes_kernel(const float *__restri
                                                            const float *__restrict__ g, const float *__restrict__ u,
                                                            __nv_bfloat16 *__restrict__ dg, __nv_bfloat16 *__restrict__ du,
                                                            long long ld, long long M, long long N) {
-    const long long n = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
+    const long long n = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 4;
     pdl_wait_primary();
     pdl_launch_dependents();
     if (n >= N) return;
     const int cols = (int)min(4LL, N - n);
-    for (long long m = blockIdx.y; m < M; m += gridDim.y) {
+    for (long long m = blockIdx.y * blockDim.y + threadIdx.y; m < M; m += gridDim.y * blockDim.y) {
         float a[4], b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -409,15 +409,16 @@ cudaError_t launch_split(const Copy *c, int n, cudaStream_t s) {
         a.rows[i] = c[i].rows;
         a.cols[i] = (int)c[i].cols;
         pieces = std::max<long long>(pieces, (c[i].cols + 3) / 4);
-        rows = std::max(rows, std::min<long long>(c[i].rows, 16384));
+        rows = std::max(rows, c[i].rows);
     }
-    return launch_pdl(split_kernel, dim3((unsigned)((pieces + 127) / 128), (unsigned)rows, (unsigned)n), 128, 0, 0, s, a);
+    const RowGrid g(rows, pieces, n);
+    return launch_pdl(split_kernel, g.grid, g.block, 0, 0, s, a);
 }
 
 cudaError_t launch_dgate_planes(const float *dh, long long dhld, const float *gu, void *dg, void *du, long long ld,
                                 long long M, long long N, cudaStream_t s) {
-    const dim3 grid((unsigned)((N + 511) / 512), (unsigned)std::min<long long>(M, 16384));
-    return launch_pdl(dgate_planes_kernel, grid, 128, 0, 0, s, dh, dhld, gu, gu + M * N, static_cast<__nv_bfloat16 *>(dg),
+    const RowGrid r(M, (N + 3) / 4);
+    return launch_pdl(dgate_planes_kernel, r.grid, r.block, 0, 0, s, dh, dhld, gu, gu + M * N, static_cast<__nv_bfloat16 *>(dg),
                       static_cast<__nv_bfloat16 *>(du), ld, M, N);
 }
 

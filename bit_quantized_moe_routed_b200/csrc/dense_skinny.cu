@@ -33,16 +33,16 @@ constexpr int kMaxStages = 12;
 constexpr int kSmemMax = 108 * 1024;      // two CTAs of an SM: the next kernel's wait beside this one's
 
 struct SkinnyArgs {
-    CUtensorMap a[2], b[2];    // weights (gate / up, or segments), tokens (segments)
+    CUtensorMap a[2], b[2];    // weights (gate / up, or segments), tokens (segments, or batches)
     int T, N;                  // tokens, outputs
-    int kblocks, nseg;
+    int kblocks, nseg, nbatch;
     int nt;                    // tokens per tile: 16, 32, 64 or 128
     int ttiles;
     int split;                 // CTAs of a cluster
     int stages;
     const float *a_scale, *b_scale[2];   // per token, per weight row
-    void *out;
-    long long old;
+    void *out[2];              // per batch
+    long long old[2];
     void *keep[2];
     long long kld;
     const void *dh;
@@ -58,10 +58,11 @@ struct SkinnyArgs {
 struct SkinnyShape {
     int nt, split;
 };
-SkinnyShape skinny_shape(long long T, long long row_tiles, long long kblocks, int sms) {
+SkinnyShape skinny_shape(const Product &p, long long row_tiles, long long kblocks, int sms) {
+    const long long T = p.M;
     SkinnyShape r;
-    r.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-    const long long tiles = (T + r.nt - 1) / r.nt * row_tiles;
+    r.nt = T <= 16 && !p.a_t ? 16 : (T <= 32 && !p.a_t ? 32 : (T <= 64 ? 64 : 128));   // transposed: whole 64-element rows
+    const long long tiles = (T + r.nt - 1) / r.nt * row_tiles * p.nbatch;
     r.split = 1;
     while (r.split < (tiles <= 8 ? 8 : 4) && tiles * r.split * 2 <= sms && kblocks >= r.split * 4) r.split *= 2;
     return r;
@@ -98,7 +99,7 @@ __device__ __forceinline__ void add4(uint32_t s[4], const uint4 &v) {
         s[i] = I8 ? s[i] + w[i] : __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(w[i]));
 }
 
-template <bool I8, bool A_MN, int EPI, typename O>
+template <bool I8, bool A_MN, bool B_MN, int EPI, typename O>
 __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __grid_constant__ SkinnyArgs p) {
     constexpr int kRows = EPI == EPI_STORE ? kT : kT / 2;   // outputs of a tile
     constexpr int kKE = I8 ? 128 : 64;
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
-    const int tile = blockIdx.x / p.split, n0 = (tile / p.ttiles) * kRows, t0 = (tile % p.ttiles) * p.nt;
+    const int row_tiles = (p.N + kRows - 1) / kRows, tile = blockIdx.x / p.split;
+    const int t0 = (tile % p.ttiles) * p.nt, n0 = (tile / p.ttiles % row_tiles) * kRows, z = tile / p.ttiles / row_tiles;
     const int S = p.stages, stage_bytes = kABytes + p.nt * kRowBytes;
     const int total = p.kblocks * p.nseg, share = (total + p.split - 1) / p.split;
     const int kb0 = min(total, rank * share), kb1 = min(total, kb0 + share);
@@ -128,7 +130,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
         } else {
             tma_load_2d(st, &p.a[seg], k0, n0, &full[s]);
         }
-        tma_load_2d(st + kABytes, &p.b[seg], k0, t0, &full[s]);
+        const CUtensorMap *mb = &p.b[p.nbatch > 1 ? z : seg];
+        if (B_MN) {
+            for (int j = 0; j < p.nt / 64; ++j) tma_load_2d(st + kABytes + j * 8192, mb, t0 + 64 * j, k0, &full[s]);
+        } else {
+            tma_load_2d(st + kABytes, mb, k0, t0, &full[s]);
+        }
         ++issued;
     };
     if (threadIdx.x == 0) {
@@ -170,16 +177,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
         }
         if (abort_flag) drain_stages(full, S, issued);
     } else if (warp == 1 && lane == 0) {
-        const uint32_t id = idesc_dense<I8>(kT, p.nt, A_MN, false);
+        const uint32_t id = idesc_dense<I8>(kT, p.nt, A_MN, B_MN);
         for (int c = 0; c < kb1 - kb0; ++c) {
             const int s = c % S;
             if (!wait_cluster(&full[s], (uint32_t)((c / S) & 1), &abort_flag)) break;
             tc_fence_after();
             const uint8_t *st = smem + s * stage_bytes;
-            const uint64_t da = A_MN ? desc_mn_sw128(st, 8192) : desc_sw128(st), db = desc_sw128(st + kABytes);
+            const uint64_t da = A_MN ? desc_mn_sw128(st, 8192) : desc_sw128(st);
+            const uint64_t db = B_MN ? desc_mn_sw128(st + kABytes, 8192) : desc_sw128(st + kABytes);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                mma_one<I8>(tmem, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (32 >> 4), id, (uint32_t)(c | k) != 0);
+                mma_one<I8>(tmem, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), id,
+                             (uint32_t)(c | k) != 0);
             tc_commit(&empty[s]);
         }
         tc_commit(&done);
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
                 }
             };
             if (EPI == EPI_STORE) {
-                put(p.out, p.old, v[0]);
+                put(p.out[z], p.old[z], v[0]);
             } else if (EPI == EPI_GLU) {
                 if (!I8 && p.keep[0]) {
                     put(p.keep[0], p.kld, v[0]);
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[0][j] = silu<sizeof(O) == 2>(v[0][j]) * v[NA - 1][j];
-                put(p.out, p.old, v[0]);
+                put(p.out[0], p.old[0], v[0]);
             } else {
                 const O *dh = static_cast<const O *>(p.dh) + (long long)tok * p.dhld + n;
 #pragma unroll
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
     if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, FLAG_TIMEOUT);
 }
 
-template <bool I8, bool A_MN, int EPI, typename O>
+template <bool I8, bool A_MN, bool B_MN, int EPI, typename O>
 cudaError_t launch_t(const Product &p, cudaStream_t s) {
     constexpr int kRows = EPI == EPI_STORE ? kT : kT / 2, es = I8 ? 1 : 2, kKE = I8 ? 128 : 64;
     SkinnyArgs a{};
@@ -291,7 +300,7 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const SkinnyShape sh = skinny_shape(p.M, (p.N + kRows - 1) / kRows, (long long)a.kblocks * a.nseg, sms);
+    const SkinnyShape sh = skinny_shape(p, (p.N + kRows - 1) / kRows, (long long)a.kblocks * a.nseg, sms);
     a.nt = sh.nt;
     a.split = sh.split;
     a.ttiles = (int)((p.M + a.nt - 1) / a.nt);
@@ -299,16 +308,18 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     for (int i = 0; i < na && e == cudaSuccess; ++i)
         e = A_MN ? make_map(&a.a[i], p.b[i], p.K, p.N, p.bld[i], es, 64)
                  : make_map(&a.a[i], p.b[i], p.N, p.K, p.bld[i], es, kRows);
-    for (int i = 0; i < p.nseg && e == cudaSuccess; ++i) e = make_map(&a.b[i], p.a[i], p.M, p.K, p.ald, es, a.nt);
+    a.nbatch = p.nbatch;
+    for (int i = 0; i < std::max(p.nseg, p.nbatch) && e == cudaSuccess; ++i)
+        e = B_MN ? make_map(&a.b[i], p.a[i], p.K, p.M, p.ald, es, 64) : make_map(&a.b[i], p.a[i], p.M, p.K, p.ald, es, a.nt);
     if (e == cudaSuccess) e = status_word(&a.status);
     if (e != cudaSuccess) return e;
     a.a_scale = p.a_scale;
     for (int i = 0; i < 2; ++i) {
         a.b_scale[i] = p.b_scale[i];
         a.keep[i] = p.keep[i];
+        a.out[i] = p.out[i];
+        a.old[i] = p.old[i];
     }
-    a.out = p.out[0];
-    a.old = p.old[0];
     a.kld = p.kld;
     a.dh = p.dh;
     a.dhld = p.dhld;
@@ -316,7 +327,7 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     const int share = (a.kblocks * a.nseg + a.split - 1) / a.split;
     a.stages = std::max(1, std::min(std::min(kMaxStages, share), kSmemMax / stage));
     const size_t smem = 1024 + (size_t)std::max(a.stages * stage, a.nt * kT * 4);
-    const auto kernel = product_skinny_kernel<I8, A_MN, EPI, O>;
+    const auto kernel = product_skinny_kernel<I8, A_MN, B_MN, EPI, O>;
     {
         static std::mutex mu;
         static bool ready[64] = {};
@@ -330,35 +341,36 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
             if (dev < 64) ready[dev] = true;
         }
     }
-    const dim3 grid((unsigned)(a.ttiles * ((a.N + kRows - 1) / kRows) * a.split));
+    const dim3 grid((unsigned)(a.ttiles * ((a.N + kRows - 1) / kRows) * a.nbatch * a.split));
     return launch_pdl(kernel, grid, kThreads, smem, a.split, s, a);
 }
 
 }  // namespace
 
 // Measured: 430 ns a K block of a CTA (the feed of its 24 to 32 KB), 0.7 us for
-// the cluster's exchange.
+// the cluster's exchange, 2.5 us for the start and end of every further round.
 long long skinny_ns(const Product &p, int sms) {
     const int ke = p.in_dtype == kI8 ? 128 : 64;
     const long long rows = p.epi == EPI_STORE ? kT : kT / 2, row_tiles = (p.N + rows - 1) / rows;
     const long long kb = (p.K + ke - 1) / ke * p.nseg;
-    const SkinnyShape sh = skinny_shape(p.M, row_tiles, kb, sms);
-    const long long tiles = (p.M + sh.nt - 1) / sh.nt * row_tiles;
-    return (tiles * sh.split + sms - 1) / sms * ((kb + sh.split - 1) / sh.split) * 430 + 700;
+    const SkinnyShape sh = skinny_shape(p, row_tiles, kb, sms);
+    const long long tiles = (p.M + sh.nt - 1) / sh.nt * row_tiles * p.nbatch;
+    const long long rounds = (tiles * sh.split + sms - 1) / sms;
+    return rounds * ((kb + sh.split - 1) / sh.split) * 430 + 700 + (rounds - 1) * 2500;
 }
 
 cudaError_t launch_product_skinny(const Product &p, cudaStream_t s) {
     typedef __nv_bfloat16 B;
     if (p.in_dtype == kI8) {
         if (p.epi == EPI_GLU)
-            return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, false, EPI_GLU, float>(p, s)
-                                               : launch_t<true, false, EPI_GLU, B>(p, s);
-        return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, false, EPI_STORE, float>(p, s)
-                                           : launch_t<true, false, EPI_STORE, B>(p, s);
+            return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, false, false, EPI_GLU, float>(p, s)
+                                               : launch_t<true, false, false, EPI_GLU, B>(p, s);
+        return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, false, false, EPI_STORE, float>(p, s)
+                                           : launch_t<true, false, false, EPI_STORE, B>(p, s);
     }
-    if (p.epi == EPI_GLU) return launch_t<false, false, EPI_GLU, B>(p, s);
-    if (p.epi == EPI_GLU_BWD) return launch_t<false, false, EPI_GLU_BWD, B>(p, s);
-    return launch_t<false, true, EPI_STORE, B>(p, s);
+    if (p.epi == EPI_GLU) return launch_t<false, false, false, EPI_GLU, B>(p, s);
+    if (p.epi == EPI_GLU_BWD) return launch_t<false, false, false, EPI_GLU_BWD, B>(p, s);
+    return p.a_t ? launch_t<false, true, true, EPI_STORE, B>(p, s) : launch_t<false, true, false, EPI_STORE, B>(p, s);
 }
 
 }  // namespace dense

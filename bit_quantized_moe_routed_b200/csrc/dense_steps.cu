@@ -18,11 +18,11 @@ struct PackArgs {
     int cols[3];                           // bytes
 };
 __global__ void __launch_bounds__(128) pack_kernel(const __grid_constant__ PackArgs p) {
-    const int z = blockIdx.z, c = (blockIdx.x * 128 + threadIdx.x) * 16;
+    const int z = blockIdx.z, c = (blockIdx.x * blockDim.x + threadIdx.x) * 16;
     pdl_wait_primary();
     pdl_launch_dependents();
     if (c >= p.cols[z]) return;
-    for (long long r = blockIdx.y; r < p.rows[z]; r += gridDim.y) {
+    for (long long r = blockIdx.y * blockDim.y + threadIdx.y; r < p.rows[z]; r += gridDim.y * blockDim.y) {
         uint32_t w[4];
         load16_any(p.src[z] + r * p.ld[z] + c, p.cols[z] - c, c > 0, w);
         *reinterpret_cast<uint4 *>(p.dst[z] + r * p.dst_ld[z] + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -35,7 +35,7 @@ typedef __nv_bfloat16 T;
 // an element each; VEC: 16 bytes of every array a thread (all rows on 16-byte
 // addresses), else one element.
 template <bool VEC>
-__global__ void __launch_bounds__(256) glu_dgate_kernel(const T *__restrict__ dh, long long dhld, const T *__restrict__ g,
+__global__ void __launch_bounds__(128) glu_dgate_kernel(const T *__restrict__ dh, long long dhld, const T *__restrict__ g,
                                                         const T *__restrict__ u, T *__restrict__ dg, T *__restrict__ du,
                                                         long long ld, long long M, long long N) {
     constexpr int kPer = VEC ? 16 / sizeof(T) : 1;
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) glu_dgate_kernel(const T *__restrict__ dh
     pdl_wait_primary();
     pdl_launch_dependents();
     if (n >= N) return;
-    for (long long m = blockIdx.y; m < M; m += gridDim.y) {
+    for (long long m = blockIdx.y * blockDim.y + threadIdx.y; m < M; m += gridDim.y * blockDim.y) {
         alignas(16) T a[kPer], b[kPer], d[kPer];
         if (VEC) {
             *reinterpret_cast<uint4 *>(a) = __ldg(reinterpret_cast<const uint4 *>(g + m * N + n));
@@ -80,9 +80,10 @@ cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s) {
         a.rows[i] = c[i].rows;
         a.cols[i] = (int)(c[i].cols * es);
         pieces = std::max<long long>(pieces, (a.cols[i] + 15) / 16);
-        rows = std::max(rows, std::min<long long>(c[i].rows, 16384));
+        rows = std::max(rows, c[i].rows);
     }
-    return launch_pdl(pack_kernel, dim3((unsigned)((pieces + 127) / 128), (unsigned)rows, (unsigned)n), 128, 0, 0, s, a);
+    const RowGrid g(rows, pieces, n);
+    return launch_pdl(pack_kernel, g.grid, g.block, 0, 0, s, a);
 }
 
 cudaError_t launch_glu_dgate(const void *dh_, long long dhld, const void *gu_, void *dg_, void *du_, long long ld,
@@ -91,9 +92,8 @@ cudaError_t launch_glu_dgate(const void *dh_, long long dhld, const void *gu_, v
     T *dg = static_cast<T *>(dg_), *du = static_cast<T *>(du_);   // the workspace's aligned planes
     constexpr int kPer = 16 / sizeof(T);
     const bool vec = !((uintptr_t)dh & 15u) && !(dhld % kPer) && !((uintptr_t)gu & 15u) && !(N % kPer);
-    const long long per = vec ? 256 * kPer : 256;
-    const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)std::min<long long>(M, 32768));
-    return launch_pdl(vec ? glu_dgate_kernel<true> : glu_dgate_kernel<false>, grid, 256, 0, 0, s, dh, dhld, gu, gu + M * N,
+    const RowGrid r(M, vec ? N / kPer : N);
+    return launch_pdl(vec ? glu_dgate_kernel<true> : glu_dgate_kernel<false>, r.grid, r.block, 0, 0, s, dh, dhld, gu, gu + M * N,
                       dg, du, ld, M, N);
 }
 

@@ -160,7 +160,7 @@ SIZES = [  # T, K, N, pad, off
     (16, 1024, 384, 0, 0), (17, 272, 200, 0, 0), (31, 640, 1000, 0, 0), (64, 4096, 2048, 0, 0), (65, 384, 300, 32, 0),
     (128, 2048, 512, 0, 0), (129, 640, 257, 0, 0), (200, 130, 64, 3, 0), (256, 128, 256, 0, 0), (257, 1000, 517, 0, 0),
     (511, 777, 640, 0, 0), (777, 1111, 1003, 5, 0), (1024, 1024, 1024, 0, 0), (1500, 64, 72, 0, 0), (2048, 33, 128, 0, 0),
-    (2048, 4096, 2048, 0, 0),
+    (2048, 4096, 2048, 0, 0), (4097, 70, 66, 0, 0), (8192, 64, 200, 8, 0), (6000, 200, 16, 0, 0),
 ]
 
 
