@@ -32,41 +32,55 @@ __global__ void __launch_bounds__(128) pack_kernel(const __grid_constant__ PackA
 typedef __nv_bfloat16 T;
 
 // dg, du from kept projections.  Bandwidth bound: three reads and two writes of
-// an element each; VEC: 16 bytes of every array a thread (all rows on 16-byte
-// addresses), else one element.
+// an element each, eight elements a thread (VEC: rows on 16-byte addresses, else
+// words shifted into place).
 template <bool VEC>
 __global__ void __launch_bounds__(128) glu_dgate_kernel(const T *__restrict__ dh, long long dhld, const T *__restrict__ g,
                                                         const T *__restrict__ u, T *__restrict__ dg, T *__restrict__ du,
                                                         long long ld, long long M, long long N) {
-    constexpr int kPer = VEC ? 16 / sizeof(T) : 1;
-    const long long n = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
+    const long long n = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 8;
     pdl_wait_primary();
     pdl_launch_dependents();
     if (n >= N) return;
+    const int left = (int)min(8LL, N - n) * 2;   // bytes of the row; the rest of the padded row gets zeros' gradients
     for (long long m = blockIdx.y * blockDim.y + threadIdx.y; m < M; m += gridDim.y * blockDim.y) {
-        alignas(16) T a[kPer], b[kPer], d[kPer];
-        if (VEC) {
-            *reinterpret_cast<uint4 *>(a) = __ldg(reinterpret_cast<const uint4 *>(g + m * N + n));
-            *reinterpret_cast<uint4 *>(b) = __ldg(reinterpret_cast<const uint4 *>(u + m * N + n));
-            *reinterpret_cast<uint4 *>(d) = __ldg(reinterpret_cast<const uint4 *>(dh + m * dhld + n));
-        } else {
-            a[0] = g[m * N + n], b[0] = u[m * N + n], d[0] = dh[m * dhld + n];
+        uint32_t a[4], b[4], d[4];
+        auto read = [&](const T *p, uint32_t w[4]) {
+            if (VEC) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {   // up to 4 bytes of the row beyond the 16: whole words where they are there
+                load16_any(reinterpret_cast<const uint8_t *>(p), (int)min(32LL, (N - n) * 2), n > 0, w);
+            }
+        };
+        read(g + m * N + n, a);
+        read(u + m * N + n, b);
+        read(dh + m * dhld + n, d);
+        if (!VEC && left < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t keep = 4 * i + 4 <= left ? 0xFFFFFFFFu : (4 * i + 2 <= left ? 0xFFFFu : 0u);
+                a[i] &= keep, b[i] &= keep, d[i] &= keep;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            float x, y;
-            glu_grad<true>((float)a[i], (float)b[i], (float)d[i], x, y);
-            st_elem(a + i, x);
-            st_elem(b + i, y);
+        for (int i = 0; i < 4; ++i) {
+            float x[2], y[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sh = 16 * h;
+                glu_grad<true>(bf16_bits_to_f32(a[i] >> sh & 0xFFFFu), bf16_bits_to_f32(b[i] >> sh & 0xFFFFu),
+                               bf16_bits_to_f32(d[i] >> sh & 0xFFFFu), x[h], y[h]);
+            }
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[0], x[1]), q = __floats2bfloat162_rn(y[0], y[1]);
+            a[i] = *reinterpret_cast<const uint32_t *>(&p);
+            b[i] = *reinterpret_cast<const uint32_t *>(&q);
         }
-        if (VEC) {
-            *reinterpret_cast<uint4 *>(dg + m * ld + n) = *reinterpret_cast<const uint4 *>(a);
-            *reinterpret_cast<uint4 *>(du + m * ld + n) = *reinterpret_cast<const uint4 *>(b);
-        } else {
-            dg[m * ld + n] = a[0], du[m * ld + n] = b[0];
-        }
+        *reinterpret_cast<uint4 *>(dg + m * ld + n) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4 *>(du + m * ld + n) = make_uint4(b[0], b[1], b[2], b[3]);
     }
 }
+
 }  // namespace
 
 cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s) {
@@ -90,9 +104,8 @@ cudaError_t launch_glu_dgate(const void *dh_, long long dhld, const void *gu_, v
                              long long M, long long N, cudaStream_t s) {
     const T *dh = static_cast<const T *>(dh_), *gu = static_cast<const T *>(gu_);
     T *dg = static_cast<T *>(dg_), *du = static_cast<T *>(du_);   // the workspace's aligned planes
-    constexpr int kPer = 16 / sizeof(T);
-    const bool vec = !((uintptr_t)dh & 15u) && !(dhld % kPer) && !((uintptr_t)gu & 15u) && !(N % kPer);
-    const RowGrid r(M, vec ? N / kPer : N);
+    const bool vec = !((uintptr_t)dh & 15u) && !(dhld % 8) && !((uintptr_t)gu & 15u) && !(N % 8);
+    const RowGrid r(M, (N + 7) / 8);
     return launch_pdl(vec ? glu_dgate_kernel<true> : glu_dgate_kernel<false>, r.grid, r.block, 0, 0, s, dh, dhld, gu, gu + M * N,
                       dg, du, ld, M, N);
 }

@@ -6,15 +6,16 @@
 // its warps split K.  A lane loads 32 consecutive bytes of a row, which are
 // the A fragments of four tensor-core steps under a permutation of K that x
 // shares (the sum does not depend on the order of K), so the weights go from
-// HBM to mma.sync without shared memory, kChunk blocks of 128 bytes of K (2
-// kChunk loads of 32 bytes a lane) always in flight.  The tokens are the N = 8 columns of
+// HBM to mma.sync without shared memory, kChunk = 4 blocks of 128 bytes of K (8
+// loads of 32 bytes a lane) always in flight.  The tokens are the N = 8 columns of
 // a step, two steps for up to 16.  tcgen05 would need the weights in shared memory first and pads N
 // to its M; at 8 columns the legacy path leaves the tensor cores far from
 // their limit.  A lane ends with the gate and the up sum of the same outputs;
 // the warps' partial sums meet in shared memory in a fixed order.
 //
 // Operands at any address and row stride: rows on 32 bytes are read 32 bytes
-// at a time, rows on 16 bytes 16, others in aligned 4-byte words and shifted.
+// at a time, rows on 16 bytes 16, others in the three aligned 16-byte pieces
+// around the 32 bytes, shifted into place.
 #include <type_traits>
 
 #include "dense_tc.cuh"
@@ -24,7 +25,6 @@ namespace dense {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kChunk = 4;      // 128-byte blocks of K a warp has in flight
 
 struct StreamArgs {
     const uint8_t *w[2];
@@ -40,31 +40,67 @@ struct StreamArgs {
     long long kld;
 };
 
-// The 32 bytes a lane takes of a row's 128-byte block.  ALIGN: 32 or 16 (base,
-// row stride and row length are multiples of it, so a piece is inside the row
-// or not) or 0 (anything).
+// The 32 bytes a lane takes of a row's 128-byte block, `left` of which (any
+// value) are in the row; zeros beyond.  ALIGN: 32 or 16 (base, row stride and
+// row length are multiples of it, so a piece is inside the row or not) or 0
+// (anything; before / after: the bytes up to 15 before and 47 behind p are the
+// matrix's too, whatever they hold).  The loads go into kWords words and are
+// put in place by settle() when they are used: shifting them at once would wait
+// for each in turn (24 against 17 us at 1 x 4095 x 2048).
 template <int ALIGN>
-__device__ __forceinline__ void load32(const uint8_t *p, int left, bool before, uint32_t w[8]) {
-    if (ALIGN == 0) {
-        load16_any(p, left, before, w);
-        load16_any(p + 16, left - 16, true, w + 4);
-        return;
+struct Piece {
+    static constexpr int kWords = ALIGN ? 8 : 12;
+    uint32_t v[kWords];
+    __device__ __forceinline__ static bool whole(const uint8_t *p, int left, bool before, bool after) {
+        const int off = (int)((uintptr_t)p & 15);
+        return left > 0 && (after || left >= 48 - off) && (before || !off);
     }
+    __device__ __forceinline__ void load(const uint8_t *p, int left, bool before, bool after) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 0;
-    if (ALIGN == 32 && left > 0)
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p));
-    if (ALIGN == 16) {
+        for (int i = 0; i < kWords; ++i) v[i] = 0;
+        if (ALIGN == 32 && left > 0)
+            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                         : "l"(p));
+        if (ALIGN == 16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (left > 16 * h) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + h);
-                w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+            for (int h = 0; h < 2; ++h)
+                if (left > 16 * h) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p) + h);
+                    v[4 * h] = q.x, v[4 * h + 1] = q.y, v[4 * h + 2] = q.z, v[4 * h + 3] = q.w;
+                }
+        }
+        if (ALIGN == 0 && whole(p, left, before, after)) {
+            const uint4 *a = reinterpret_cast<const uint4 *>((uintptr_t)p & ~(uintptr_t)15);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const uint4 q = __ldg(a + i);
+                v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
             }
+        }
     }
-}
+    __device__ __forceinline__ void settle(const uint8_t *p, int left, bool before, bool after) {
+        if (ALIGN) return;
+        if (left <= 0) return;   // zeros
+        if (!whole(p, left, before, after)) {
+            load16_any(p, left, before, v);
+            load16_any(p + 16, left - 16, true, v + 4);
+            return;
+        }
+        const int off = (int)((uintptr_t)p & 15);
+        const bool two = off & 8, one = off & 4;
+#pragma unroll
+        for (int i = 0; i < 10; ++i) v[i] = two ? v[(i + 2) % kWords] : v[i];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) v[i] = one ? v[(i + 1) % kWords] : v[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = left - 4 * i;
+            v[i] = __funnelshift_r(v[i], v[(i + 1) % kWords], 8 * (off & 3)) &
+                   (n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u));
+        }
+    }
+};
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
@@ -89,6 +125,7 @@ template <bool I8, int EPI, int ALIGN, int NT, typename O>
 __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __grid_constant__ StreamArgs p) {
     typedef typename Sum<I8>::type E;
     __shared__ E part[kWarps][NT][4][32];
+    constexpr int kChunk = ALIGN ? 4 : 2;                 // 128-byte blocks of K a warp has in flight
     constexpr int kAhead = NT == 1 ? 2 : 1;               // blocks by which the tokens are loaded ahead
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int per = EPI == EPI_STORE ? 16 : 8;            // outputs of a group
@@ -103,19 +140,27 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
     for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0;
     const int blocks = (p.kbytes + 127) / 128, share = (blocks + kWarps - 1) / kWarps;
     const int b_first = warp * share, b_end = min(blocks, (warp + 1) * share);
-    uint32_t a[kChunk][2][8], xr[kAhead][NT][8];
-    auto load_w = [&](int j, int b) {
+    Piece<ALIGN> a[kChunk][2], xr[kAhead][NT];
+    // unaligned rows: whether other rows of the matrix lie before and behind this
+    // lane's (strides of 48 bytes at least)
+    const bool wide0 = p.ldw[0] >= 48, wide1 = (EPI == EPI_STORE ? p.ldw[0] : p.ldw[1]) >= 48;
+    auto of_w = [&](int b, auto f0, auto f1) {   // f(address, bytes left, before, after) of this lane's rows at block b
         const int k = b * 128 + 32 * t;
         const bool in = b < b_end;
-        load32<ALIGN>(w0 + k, in ? k0 - k : 0, k > 0, a[j][0]);
-        load32<ALIGN>(w1 + k, in ? k1 - k : 0, k > 0, a[j][1]);
+        f0(w0 + k, in ? k0 - k : 0, k > 0 || (wide0 && r0 > 0), wide0 && r0 < p.N - 1);
+        f1(w1 + k, in ? k1 - k : 0, k > 0 || (wide1 && r1 > 0), wide1 && r1 < p.N - 1);
+    };
+    auto of_x = [&](int b, int i, auto f) {
+        const int k = b * 128 + 32 * t, tok = 8 * i + g;
+        f(p.x + (long long)min(tok, p.T - 1) * p.ldx + k, b < b_end && tok < p.T ? p.kbytes - k : 0,
+          k > 0 || (p.ldx >= 48 && tok > 0), p.ldx >= 48 && tok < p.T - 1);
+    };
+    auto load_w = [&](int j, int b) {
+        of_w(b, [&](auto... v) { a[j][0].load(v...); }, [&](auto... v) { a[j][1].load(v...); });
     };
     auto load_x = [&](int j, int b) {
-        const int k = b * 128 + 32 * t;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            load32<ALIGN>(p.x + (long long)min(8 * i + g, p.T - 1) * p.ldx + k,
-                          b < b_end && 8 * i + g < p.T ? p.kbytes - k : 0, k > 0, xr[j][i]);
+        for (int i = 0; i < NT; ++i) of_x(b, i, [&](auto... v) { xr[j][i].load(v...); });
     };
     // the first blocks on their way to L2 while the kernel before drains
 #pragma unroll
@@ -133,12 +178,14 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
     for (int b0 = b_first; b0 < b_end; b0 += kChunk) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {   // a block past the share's end is zeros on both sides
+            of_w(b0 + j, [&](auto... v) { a[j][0].settle(v...); }, [&](auto... v) { a[j][1].settle(v...); });
+            const uint32_t *w = a[j][0].v, *u = a[j][1].v;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const uint32_t *x = xr[j % kAhead][i];
+                of_x(b0 + j, i, [&](auto... v) { xr[j % kAhead][i].settle(v...); });
+                const uint32_t *x = xr[j % kAhead][i].v;
 #pragma unroll
-                for (int q = 0; q < 8; q += 2)
-                    step(c[i], a[j][0][q], a[j][1][q], a[j][0][q + 1], a[j][1][q + 1], x[q], x[q + 1]);
+                for (int q = 0; q < 8; q += 2) step(c[i], w[q], u[q], w[q + 1], u[q + 1], x[q], x[q + 1]);
             }
             load_w(j, b0 + kChunk + j);
             load_x(j % kAhead, b0 + kAhead + j);
