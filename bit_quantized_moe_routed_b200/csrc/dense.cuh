@@ -176,7 +176,8 @@ struct PlanesProduct {   // as Product
     long long dhld = 0;
     int epi = EPI_STORE;
 };
-cudaError_t launch_product_planes(const PlanesProduct &p, cudaStream_t s);
+cudaError_t launch_product_planes(const PlanesProduct &p, cudaStream_t s);              // the gated block
+cudaError_t launch_gradients_planes(const PlanesProduct *p, int n, cudaStream_t s);    // dx, dW, or both in one launch
 cudaError_t launch_split(const Copy *c, int n, cudaStream_t s);   // dst: planes
 cudaError_t launch_dgate_planes(const float *dh, long long dhld, const float *gu, void *dg, void *du, long long ld,
                                 long long M, long long N, cudaStream_t s);

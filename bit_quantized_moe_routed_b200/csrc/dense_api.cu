@@ -411,9 +411,11 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         pw.old[i] = a->lddw[i];
     }
     if (plan.planes) {
-        if (a->dx) e = launch_product_planes(of_planes(px), s);
-        if (a->dw[0] && e == cudaSuccess) e = launch_product_planes(of_planes(pw), s);
-        return done(e);
+        PlanesProduct both[2];
+        int n = 0;
+        if (a->dx) both[n++] = of_planes(px);
+        if (a->dw[0]) both[n++] = of_planes(pw);
+        return done(launch_gradients_planes(both, n, s));
     }
     return done(launch_gradients(a->dx ? &px : nullptr, a->dw[0] ? &pw : nullptr, s));
 }

@@ -41,13 +41,18 @@ constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 constexpr int kChunk = 2;                        // K blocks of a hi hi sum
 constexpr int kTmem = 256;                       // columns: hi hi twice, the small products, unused
 
-struct PlanesArgs {
+struct PlanesWork {
     CUtensorMap a[2], b[2];    // A: gate / up, or segments; B: segments, or batches
     long long M, N;            // rows of B (rows of out), rows of A (columns of out)
     int kblocks, nseg, nbatch;
-    int mtiles, split;
+    int mtiles, ntiles, split; // split: CTAs that share a tile's K
+    bool b_mn;                 // B stored [K][M]
     void *out[2];
     long long old[2];
+};
+struct PlanesArgs {
+    PlanesWork w[2];           // dx and dW in one launch, or one work
+    int clusters0, size;       // clusters of work 0; CTAs of a cluster: size / split tiles of a work
     void *keep[2];             // EPI_GLU: f32; EPI_GLU_BWD: planes
     long long kld, kplane;
     const float *dh;
@@ -101,8 +106,9 @@ __device__ __forceinline__ void put_planes(__nv_bfloat16 *d, long long plane, co
             if (j < cols) d[q * plane + j] = p[j][q];
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+template <int EPI>
 __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __grid_constant__ PlanesArgs p) {
+    constexpr bool A_MN = EPI == EPI_STORE;                 // dx, dW: A stored [K][N]
     constexpr int kRows = EPI == EPI_STORE ? kT : kT / 2;   // outputs (columns of out) of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -110,12 +116,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = p.split > 1 ? (int)cluster_rank() : 0;
-    int tile = blockIdx.x / p.split;
-    const int m0 = tile % p.mtiles * kNT;
-    tile /= p.mtiles;
-    const int ntiles = (int)((p.N + kRows - 1) / kRows), n0 = tile % ntiles * kRows, z = tile / ntiles;
-    const int total = p.kblocks * p.nseg, share = (total + p.split - 1) / p.split;
+    const int in_cluster = p.size > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / p.size;
+    const PlanesWork &w = p.w[cluster >= p.clusters0];
+    const bool b_mn = A_MN && w.b_mn;
+    const int split = w.split, rank = in_cluster % split, first = in_cluster - rank;   // first: the tile's first CTA
+    int tile = (cluster >= p.clusters0 ? cluster - p.clusters0 : cluster) * (p.size / split) + in_cluster / split;
+    const bool live = tile < w.mtiles * w.ntiles * w.nbatch;   // a cluster's last tiles may not be there
+    const int m0 = tile % w.mtiles * kNT;
+    tile /= w.mtiles;
+    const int n0 = tile % w.ntiles * kRows, z = live ? tile / w.ntiles : 0;
+    const int total = live ? w.kblocks * w.nseg : 0, share = (total + split - 1) / split;
     const int kb0 = min(total, rank * share), kbs = min(total, kb0 + share) - kb0;
     const int chunks = (kbs + kChunk - 1) / kChunk;
     if (threadIdx.x == 0) {
@@ -145,27 +155,28 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
     if (warp == 0 && lane == 0) {
         int c = 0;
         for (; c < kbs; ++c) {
-            const int s = c % kStages, kb = kb0 + c, seg = p.nseg > 1 && kb >= p.kblocks, k0 = (seg ? kb - p.kblocks : kb) * 64;
+            const int s = c % kStages, kb = kb0 + c, seg = w.nseg > 1 && kb >= w.kblocks, k0 = (seg ? kb - w.kblocks : kb) * 64;
             if (c >= kStages && !wait_cluster(&empty[s], (uint32_t)((c / kStages - 1) & 1), &abort_flag)) break;
             uint8_t *sa = smem + s * kStage, *sb = sa + kABytes;
             mbar_arrive_expect_tx(&full[s], kStage);
             if (A_MN) {   // [64 columns][plane][64 rows of K]
-                tma_load_3d(sa, &p.a[seg], n0, k0, 0, &full[s]);
-                tma_load_3d(sa + kABytes / 2, &p.a[seg], n0 + 64, k0, 0, &full[s]);
+                tma_load_3d(sa, &w.a[seg], n0, k0, 0, &full[s]);
+                tma_load_3d(sa + kABytes / 2, &w.a[seg], n0 + 64, k0, 0, &full[s]);
             } else {      // [plane][gate rows, up rows]
 #pragma unroll
                 for (int q = 0; q < 3; ++q)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        tma_load_3d(sa + q * (kABytes / 3) + h * (kABytes / 6), &p.a[h], k0, n0, q, &full[s]);
+                        tma_load_3d(sa + q * (kABytes / 3) + h * (kABytes / 6), &w.a[h], k0, n0, q, &full[s]);
             }
-            const CUtensorMap *mb = &p.b[p.nbatch > 1 ? z : seg];
-            if (B_MN) tma_load_3d(sb, mb, m0, k0, 0, &full[s]);
+            const CUtensorMap *mb = &w.b[w.nbatch > 1 ? z : seg];
+            if (b_mn) tma_load_3d(sb, mb, m0, k0, 0, &full[s]);
             else tma_load_3d(sb, mb, k0, m0, 0, &full[s]);
         }
         if (abort_flag) drain_stages(full, kStages, c);
     } else if (warp == 1 && lane == 0) {
-        constexpr uint32_t id = idesc_dense<false>(kT, kNT, A_MN, B_MN);
+        const uint32_t id = b_mn ? idesc_dense<false>(kT, kNT, A_MN, true) : idesc_dense<false>(kT, kNT, A_MN, false);
+        const uint64_t bstep = b_mn ? 2048 >> 4 : 32 >> 4;
         bool ok = true;
         for (int c = 0; ok && c < kbs; ++c) {
             const int s = c % kStages, q = c / kChunk, buf = q & 1;
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 da[i] = A_MN ? desc_mn_sw128(sa + i * 8192, kABytes / 2) : desc_sw128(sa + i * (kABytes / 3));
-                db[i] = B_MN ? desc_mn_sw128(sb + i * 8192, 8192) : desc_sw128(sb + i * 8192);
+                db[i] = b_mn ? desc_mn_sw128(sb + i * 8192, 8192) : desc_sw128(sb + i * 8192);
             }
             // (part of A, part of B): the small products, then hi hi
             constexpr int pa[6] = {1, 0, 2, 0, 1, 0}, pb[6] = {1, 2, 0, 1, 0, 0};
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_bf16(o == 5 ? tmem + buf * kNT : tmem + 2 * kNT, da[pa[o]] + k * (A_MN ? 2048 >> 4 : 32 >> 4),
-                             db[pb[o]] + k * (B_MN ? 2048 >> 4 : 32 >> 4), id,
+                             db[pb[o]] + k * bstep, id,
                              o == 5 ? (uint32_t)(c % kChunk | k) != 0 : (uint32_t)(c | o | k) != 0);
             tc_commit(&empty[s]);
             if (c % kChunk == kChunk - 1 || c == kbs - 1) tc_commit(&main_full[buf]);
@@ -235,33 +246,33 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
         tc_fence_after();
         tc_dealloc(tmem, kTmem);
     }
-    if (p.split > 1) cluster_sync();
+    if (p.size > 1) cluster_sync();
 
     // ---- this CTA's share of the rows of out: four columns a lane
     constexpr int NA = EPI == EPI_STORE ? 1 : 2, kLanes = kRows / 4;
-    const int per = kNT / p.split;
+    const int per = live ? kNT / split : 0;
     for (int i = threadIdx.x / kLanes; i < per; i += kThreads / kLanes) {
         const int lm = rank * per + i, r4 = (threadIdx.x % kLanes) * 4;
         const long long m = m0 + lm, n = n0 + r4;
-        const int cols = (int)min(4LL, p.N - n);
-        if (m >= p.M) continue;
+        const int cols = (int)min(4LL, w.N - n);
+        if (m >= w.M) continue;
         float v[NA][4] = {};
-        for (int r = 0; r < p.split; ++r)
+        for (int r = 0; r < split; ++r)
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
                 const float *src = part + lm * kT + a * kRows + r4;
-                const float4 w = p.split > 1 ? ld_cluster_f4(in_cta(src, r)) : *reinterpret_cast<const float4 *>(src);
-                v[a][0] += w.x, v[a][1] += w.y, v[a][2] += w.z, v[a][3] += w.w;
+                const float4 q = split > 1 ? ld_cluster_f4(in_cta(src, first + r)) : *reinterpret_cast<const float4 *>(src);
+                v[a][0] += q.x, v[a][1] += q.y, v[a][2] += q.z, v[a][3] += q.w;
             }
-        auto put = [&](void *dst, long long ld, const float *w) {
+        auto put = [&](void *dst, long long ld, const float *q) {
             float *d = static_cast<float *>(dst) + m * ld + n;
-            if (cols == 4 && !((uintptr_t)d & 15u)) *reinterpret_cast<float4 *>(d) = make_float4(w[0], w[1], w[2], w[3]);
+            if (cols == 4 && !((uintptr_t)d & 15u)) *reinterpret_cast<float4 *>(d) = make_float4(q[0], q[1], q[2], q[3]);
             else
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (j < cols) d[j] = w[j];
+                    if (j < cols) d[j] = q[j];
         };
-        if (EPI == EPI_STORE) put(p.out[z], p.old[z], v[0]);
+        if (EPI == EPI_STORE) put(w.out[z], w.old[z], v[0]);
         if (EPI == EPI_GLU) {
             if (p.keep[0]) {
                 put(p.keep[0], p.kld, v[0]);
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[0][j] = silu<false>(v[0][j]) * v[NA - 1][j];
-            put(p.out[0], p.old[0], v[0]);
+            put(w.out[0], w.old[0], v[0]);
         }
         if (EPI == EPI_GLU_BWD) {
 #pragma unroll
@@ -281,45 +292,60 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
         }
     }
     __syncwarp();
-    if (p.split > 1)   // no CTA leaves while another reads its shared memory
+    if (p.size > 1)   // no CTA leaves while another reads its shared memory
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, FLAG_TIMEOUT);
 }
 
-template <bool A_MN, bool B_MN, int EPI>
-cudaError_t launch_t(const PlanesProduct &p, cudaStream_t s) {
+template <int EPI>
+cudaError_t launch_t(const PlanesProduct *ps, int nwork, cudaStream_t s) {
     constexpr int kRows = EPI == EPI_STORE ? kT : kT / 2;
     PlanesArgs a{};
-    const int na = EPI == EPI_STORE ? p.nseg : 2, nb = std::max(p.nseg, p.nbatch);
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < na && e == cudaSuccess; ++i)
-        e = A_MN ? make_planes_map(&a.a[i], p.b[i], 64, 3) : make_planes_map(&a.a[i], p.b[i], kRows, 1);
-    for (int i = 0; i < nb && e == cudaSuccess; ++i) e = make_planes_map(&a.b[i], p.a[i], 64, 3);
-    if (e == cudaSuccess) e = status_word(&a.status);
     int sms = 0;
+    cudaError_t e = status_word(&a.status);
     if (e == cudaSuccess) e = sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    a.M = p.M;
-    a.N = p.N;
-    a.kblocks = (int)((p.K + 63) / 64);
-    a.nseg = p.nseg;
-    a.nbatch = p.nbatch;
-    a.mtiles = (int)((p.M + kNT - 1) / kNT);
-    const long long tiles = (long long)a.mtiles * ((p.N + kRows - 1) / kRows) * p.nbatch;
-    const long long kb = (long long)a.kblocks * a.nseg;
-    a.split = 1;
-    while (a.split < (tiles <= 8 ? 8 : 4) && tiles * a.split * 2 <= sms && kb >= a.split * 2) a.split *= 2;
-    if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    for (int i = 0; i < 2; ++i) {
-        a.out[i] = p.out[i];
-        a.old[i] = p.old[i];
-        a.keep[i] = p.keep[i];
+    a.size = 1;
+    for (int j = 0; j < nwork && e == cudaSuccess; ++j) {
+        const PlanesProduct &p = ps[j];
+        PlanesWork &w = a.w[j];
+        const int na = EPI == EPI_STORE ? p.nseg : 2, nb = std::max(p.nseg, p.nbatch);
+        for (int i = 0; i < na && e == cudaSuccess; ++i)
+            e = EPI == EPI_STORE ? make_planes_map(&w.a[i], p.b[i], 64, 3) : make_planes_map(&w.a[i], p.b[i], kRows, 1);
+        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = make_planes_map(&w.b[i], p.a[i], 64, 3);
+        w.M = p.M;
+        w.N = p.N;
+        w.kblocks = (int)((p.K + 63) / 64);
+        w.nseg = p.nseg;
+        w.nbatch = p.nbatch;
+        w.b_mn = p.a_t;
+        w.mtiles = (int)((p.M + kNT - 1) / kNT);
+        w.ntiles = (int)((p.N + kRows - 1) / kRows);
+        const long long tiles = (long long)w.mtiles * w.ntiles * p.nbatch;
+        if (tiles > 0x0FFFFFFF) return cudaErrorInvalidConfiguration;
+        // of its own sizes alone: what else a launch computes changes no bits
+        w.split = 1;
+        while (w.split < (tiles <= 8 ? 8 : 4) && tiles * w.split * 2 <= sms && (long long)w.kblocks * w.nseg >= w.split * 2)
+            w.split *= 2;
+        a.size = std::max(a.size, w.split);
+        for (int i = 0; i < 2; ++i) {
+            w.out[i] = p.out[i];
+            w.old[i] = p.old[i];
+        }
     }
+    if (e != cudaSuccess) return e;
+    long long clusters = 0;
+    for (int j = 0; j < nwork; ++j) {
+        const int per = a.size / a.w[j].split, tiles = a.w[j].mtiles * a.w[j].ntiles * a.w[j].nbatch;
+        clusters += (tiles + per - 1) / per;
+        if (j == 0) a.clusters0 = (int)clusters;
+    }
+    const PlanesProduct &p = ps[0];
+    for (int i = 0; i < 2; ++i) a.keep[i] = p.keep[i];
     a.kld = p.kld;
     a.kplane = p.kplane;
     a.dh = p.dh;
     a.dhld = p.dhld;
-    const auto kernel = product_planes_kernel<A_MN, B_MN, EPI>;
+    const auto kernel = product_planes_kernel<EPI>;
     {
         static std::mutex mu;
         static bool ready[64] = {};
@@ -333,7 +359,7 @@ cudaError_t launch_t(const PlanesProduct &p, cudaStream_t s) {
             if (dev < 64) ready[dev] = true;
         }
     }
-    return launch_pdl(kernel, dim3((unsigned)(tiles * a.split)), kThreads, kSmem, a.split, s, a);
+    return launch_pdl(kernel, dim3((unsigned)(clusters * a.size)), kThreads, kSmem, a.size, s, a);
 }
 
 struct SplitArgs {
@@ -423,10 +449,9 @@ cudaError_t launch_dgate_planes(const float *dh, long long dhld, const float *gu
 }
 
 cudaError_t launch_product_planes(const PlanesProduct &p, cudaStream_t s) {
-    if (p.epi == EPI_GLU) return launch_t<false, false, EPI_GLU>(p, s);
-    if (p.epi == EPI_GLU_BWD) return launch_t<false, false, EPI_GLU_BWD>(p, s);
-    return p.a_t ? launch_t<true, true, EPI_STORE>(p, s) : launch_t<true, false, EPI_STORE>(p, s);
+    return p.epi == EPI_GLU ? launch_t<EPI_GLU>(&p, 1, s) : launch_t<EPI_GLU_BWD>(&p, 1, s);
 }
+cudaError_t launch_gradients_planes(const PlanesProduct *p, int n, cudaStream_t s) { return launch_t<EPI_STORE>(p, n, s); }
 
 }  // namespace dense
 }  // namespace moeq
