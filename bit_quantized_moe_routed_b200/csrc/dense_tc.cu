@@ -350,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 } else {
                     if constexpr (sizeof(O) == 2) {
                         float d[32];
-                        load_32x32(stage, d, static_cast<const O *>(p.dh) + m0 * p.dhld + n, p.dhld, rows, cols, p.vec_dh);
+                        load_32x32(d, static_cast<const O *>(p.dh) + m0 * p.dhld + n, p.dhld, rows, w.N - n, n > 0, p.vec_dh);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) glu_grad<true>(g[i], u[i], d[i], g[i], u[i]);
                     }

@@ -145,25 +145,22 @@ __device__ __forceinline__ void store_32x32(uint8_t *stage, const float v[32], O
             dst[(long long)r * ld + lane] = *reinterpret_cast<const O *>(stage + slot(r, lane / kPer) + lane % kPer * sizeof(O));
     }
 }
-// The reverse for bf16: 32 x 32 elements at src, this lane's row into v (zeros outside).
-__device__ __forceinline__ void load_32x32(uint8_t *stage, float v[32], const __nv_bfloat16 *src, long long ld, int rows,
-                                           int cols, bool vec) {
+// A lane's row of 32 x 32 bf16 elements at src into v, zeros outside.  left:
+// elements of a row from src on; before: whether a row has some before src.
+__device__ __forceinline__ void load_32x32(float v[32], const __nv_bfloat16 *src, long long ld, int rows, long long left,
+                                           bool before, bool vec) {
     const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *row = src + (long long)(lane < rows ? lane : 0) * ld;
     uint4 w[4];
-    if (vec && cols == 32) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            w[c] = lane < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (long long)lane * ld) + c) : make_uint4(0, 0, 0, 0);
-    } else {
-        auto slot = [&](int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
-        __syncwarp();
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r)
-            *reinterpret_cast<uint16_t *>(stage + slot(r, lane >> 3) + (lane & 7) * 2) =
-                r < rows && lane < cols ? __ldg(reinterpret_cast<const uint16_t *>(src + (long long)r * ld + lane)) : 0;
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4 *>(stage + slot(lane, c));
+    for (int c = 0; c < 4; ++c) {
+        const int in = lane < rows ? (int)max(0LL, min(64LL, (left - 8 * c) * 2)) : 0;   // bytes of the row
+        if (vec && in >= 16) w[c] = __ldg(reinterpret_cast<const uint4 *>(row) + c);
+        else {
+            uint32_t u[4];
+            load16_any(reinterpret_cast<const uint8_t *>(row + 8 * c), in, before || c > 0, u);
+            w[c] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
