@@ -44,7 +44,7 @@ NCU_TRAFFIC = {
                       "bit_quantized_moe_routed_b200/csrc/decode_common.cuh",
                       "bit_quantized_moe_routed_b200/csrc/internal.cuh",
                       "include/moeq.h"),
-                     "03c27e330f2b184efdba25b8c17f2e221b9a1c4f40d222a26c0d0ba8fcfe21c5",
+                     "7805bceb51b9e4b1201e42fe5ada0b7f052e0c72dcdaed1cadcd6a721c12efe6",
                      107049216.0 + 358144.0, "profiles/dec_fused_mx_decode_mxfp4.md"),
 }
 

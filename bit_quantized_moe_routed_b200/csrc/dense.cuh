@@ -138,7 +138,8 @@ cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
 // dx and dW (both weights') in one launch, either of them NULL; bf16, operands
 // as for launch_product_tc
 cudaError_t launch_gradients_tc(const Product *dx, const Product *dw, cudaStream_t s);
-// bf16 and int8, at most kStreamRows rows of A, any strides and alignment (dense_stream.cu)
+// bf16 and int8, at most kStreamRows rows of A, any strides and alignment
+// (dense_stream.cu); EPI_GLU_BWD: keep is f32, at most kFewRows rows
 constexpr int kStreamRows = 16;
 bool stream_supported(const Product &p);
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
@@ -157,6 +158,14 @@ struct Copy {
     long long dst_ld, rows, cols;
 };
 cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s);
+// bf16, at most kFewRows tokens, any strides and alignment: both gradients from
+// f32 gate gradients dg, du [T][dld] (dense_few.cu).  px, pw: dx and dW as for
+// launch_gradients_tc, either of them NULL; their A is not read.
+constexpr int kFewRows = 4;
+cudaError_t launch_few_gradients(const Product *px, const Product *pw, const float *dg, const float *du, long long dld,
+                                 cudaStream_t s);
+cudaError_t launch_dgate_f32(const void *dh, long long dhld, const void *gu, float *dg, float *du, long long ld, int T, int N,
+                             cudaStream_t s);
 // f32 products from bf16 planes (dense_planes.cu).  A matrix's planes: bf16
 // [3][rows][ld], ld a multiple of 64.
 struct Planes {

@@ -81,7 +81,7 @@ struct Packed {
 // The workspace's parts, in the order they lie in it.  planes: f32 operands are
 // multiplied as bf16 planes, which x, w and dgu then hold.
 struct Plan {
-    bool planes = false;
+    bool planes = false, few = false;   // few: dgu is f32 [2][T][dgu_ld] (dense_few.cu)
     Packed x, w[2];
     size_t dgu = 0;            // gradients of the projections, [2][T][dgu_ld] (or [2] planes of them)
     long long dgu_ld = 0;
@@ -196,10 +196,30 @@ bool glu_args_ok(const moeq_glu_args *a, bool backward) {
         if (a->dw[i] && !matrix_ok(a->dw[i], a->hidden, a->lddw[i], es)) return false;
     return true;
 }
+// The gradients of few tokens by dense_few.cu, or on the tensor cores.  Graphs of
+// back-to-back calls, us, dense_few.cu against tensor cores, 1 and 4 tokens:
+//   kept projections  512 x 517 7.1, 8.0 against 11.5, 11.3; 64 x 138 5.2, 6.2
+//     against 7.0, 7.0; 1024 x 1024 14.1, 15.1 against 13.2, 13.1
+//   recomputed  1024 x 1024 11.3, 13.6 against 16.4, 16.8; 1024 x 4096 22.7, 24.5
+//     against 42.5, 38.5; 4096 x 2048 20.3, 29.1 against 40.7, 40.7
+//   rows off 16 bytes, kept  77 x 69 6.6, 7.4 against 8.3, 8.5; 77 x 301 12.3, 12.8
+//     against 9.9, 10.0; 333 x 260 12.3, 12.7 against 10.2, 10.4.  There the
+//     limit is for accuracy: the smallest sums gain most from f32 dg and du.
+// Only what both gradients need decides, so that asking for one changes no bits.
+bool few_tokens(const moeq_glu_args *a) {
+    if (a->dtype != MOEQ_ACT_BF16 || a->n_tokens > kFewRows) return false;
+    auto rows16 = [](const void *p, long long ld) { return !((uintptr_t)p & 15u) && !(ld & 7); };
+    const bool aligned = rows16(a->x, a->ldx) && rows16(a->w[0], a->ldw[0]) && rows16(a->w[1], a->ldw[1]);
+    const long long size = (long long)a->hidden * a->inter;
+    if (!aligned) return size <= 1 << 16;
+    return a->gu ? size <= 1 << 19 : size * a->n_tokens <= 1 << 25;
+}
+
 Plan plan_glu(const moeq_glu_args *a, bool backward) {
     Plan p;
     if (a->n_tokens == 0) return p;
-    if (a->dtype == MOEQ_ACT_BF16 && (backward || a->n_tokens > kStreamRows)) {
+    p.few = backward && few_tokens(a);
+    if (a->dtype == MOEQ_ACT_BF16 && !p.few && (backward || a->n_tokens > kStreamRows)) {
         if (!backward || !a->gu || a->dw[0]) p.x = Packed(a->x, a->n_tokens, a->hidden, a->ldx, 2);
         if (!backward || !a->gu || a->dx)
             for (int i = 0; i < 2; ++i) p.w[i] = Packed(a->w[i], a->inter, a->hidden, a->ldw[i], 2);
@@ -211,7 +231,7 @@ Plan plan_glu(const moeq_glu_args *a, bool backward) {
     }
     if (!backward) return p;
     p.dgu_ld = (a->inter + 63) / 64 * 64;
-    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * (p.planes ? 6 : 2));
+    p.dgu = round256((size_t)2 * a->n_tokens * p.dgu_ld * (p.planes ? 6 : (p.few ? 4 : 2)));
     return p;
 }
 
@@ -356,8 +376,10 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
     for (int i = 0; i < 2; ++i) pk.add(plan.w[i], w[i], ldw[i], I, H);
     cudaError_t e = pk.run(s, plan.planes);
     if (e != cudaSuccess) return MOEQ_ERR_CUDA;
-    char *dg = pk.ws, *du = dg + (size_t)T * plan.dgu_ld * (plan.planes ? 6 : es);
-    if (a->gu && plan.planes) {
+    char *dg = pk.ws, *du = dg + (size_t)T * plan.dgu_ld * (plan.planes ? 6 : (plan.few ? 4 : es));
+    if (a->gu && plan.few) {
+        e = launch_dgate_f32(a->dh, a->lddh, a->gu, (float *)dg, (float *)du, plan.dgu_ld, (int)T, (int)I, s);
+    } else if (a->gu && plan.planes) {
         e = launch_dgate_planes(static_cast<const float *>(a->dh), a->lddh, static_cast<const float *>(a->gu), dg, du,
                                 plan.dgu_ld, T, I, s);
     } else if (a->gu) {
@@ -410,6 +432,9 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         pw.out[i] = a->dw[i];
         pw.old[i] = a->lddw[i];
     }
+    if (plan.few)
+        return done(launch_few_gradients(a->dx ? &px : nullptr, a->dw[0] ? &pw : nullptr, (const float *)dg,
+                                         (const float *)du, plan.dgu_ld, s));
     if (plan.planes) {
         PlanesProduct both[2];
         int n = 0;

@@ -38,6 +38,8 @@ struct StreamArgs {
     long long old;
     void *keep[2];
     long long kld;
+    const void *dh;
+    long long dhld;
 };
 
 // The 32 bytes a lane takes of a row's 128-byte block, `left` of which (any
@@ -204,13 +206,13 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             s0 += part[w][i][q][src];
-            if (EPI == EPI_GLU) s1 += part[w][i][q + 2][src];
+            if (EPI != EPI_STORE) s1 += part[w][i][q + 2][src];
         }
         float v0 = (float)s0, v1 = (float)s1;
         if (I8) {
             const float sx = __ldg(p.a_scale + tok);
             v0 = v0 * sx * __ldg(p.b_scale[0] + n);
-            if (EPI == EPI_GLU) v1 = v1 * sx * __ldg(p.b_scale[1] + n);
+            if (EPI != EPI_STORE) v1 = v1 * sx * __ldg(p.b_scale[1] + n);
         }
         O *out = static_cast<O *>(p.out) + (long long)tok * p.old + n;
         if (EPI == EPI_GLU) {
@@ -219,6 +221,11 @@ __global__ void __launch_bounds__(kThreads, 2) product_stream_kernel(const __gri
                 st_elem(static_cast<O *>(p.keep[0]) + (long long)tok * p.kld + n, v0);
                 st_elem(static_cast<O *>(p.keep[1]) + (long long)tok * p.kld + n, v1);
             }
+        } else if (EPI == EPI_GLU_BWD) {   // f32, as the gradients of few tokens take them
+            float dg, du;
+            glu_grad<false>(v0, v1, ld_elem(static_cast<const __nv_bfloat16 *>(p.dh) + (long long)tok * p.dhld + n), dg, du);
+            static_cast<float *>(p.keep[0])[(long long)tok * p.kld + n] = dg;
+            static_cast<float *>(p.keep[1])[(long long)tok * p.kld + n] = du;
         } else {
             st_elem(out, v0);
         }
@@ -231,14 +238,13 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     StreamArgs a{};
     // the alignment that every row of every operand has
     unsigned long long low = (uintptr_t)p.a[0] | (p.M > 1 ? p.ald * es : 0) | p.K * es;
-    for (int i = 0; i < (EPI == EPI_GLU ? 2 : 1); ++i) {
+    for (int i = 0; i < (EPI != EPI_STORE ? 2 : 1); ++i) {
         a.w[i] = static_cast<const uint8_t *>(p.b[i]);
         a.ldw[i] = p.bld[i] * es;
         a.b_scale[i] = p.b_scale[i];
         a.keep[i] = p.keep[i];
         low |= (uintptr_t)p.b[i] | (p.N > 1 ? a.ldw[i] : 0);
     }
-    if (EPI == EPI_GLU) a.keep[1] = p.keep[1];
     a.x = static_cast<const uint8_t *>(p.a[0]);
     a.ldx = p.ald * es;
     a.T = (int)p.M;
@@ -248,11 +254,14 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
     a.out = p.out[0];
     a.old = p.old[0];
     a.kld = p.kld;
+    a.dh = p.dh;
+    a.dhld = p.dhld;
     const int per = EPI == EPI_STORE ? 16 : 8;
     const int grid = (a.N + per - 1) / per;
     auto pick = [&](auto align) {
         constexpr int A = decltype(align)::value;
-        return a.T <= 8 ? product_stream_kernel<I8, EPI, A, 1, O> : product_stream_kernel<I8, EPI, A, 2, O>;
+        if constexpr (EPI == EPI_GLU_BWD) return product_stream_kernel<I8, EPI, A, 1, O>;
+        else return a.T <= 8 ? product_stream_kernel<I8, EPI, A, 1, O> : product_stream_kernel<I8, EPI, A, 2, O>;
     };
     const auto kernel = !(low & 31) ? pick(std::integral_constant<int, 32>{})
                                     : (!(low & 15) ? pick(std::integral_constant<int, 16>{})
@@ -263,7 +272,7 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
 }  // namespace
 
 bool stream_supported(const Product &p) {
-    return p.M <= kStreamRows && p.in_dtype != MOEQ_ACT_F32 && !p.a_t && !p.b_t && p.epi != EPI_GLU_BWD;
+    return p.M <= (p.epi == EPI_GLU_BWD ? kFewRows : kStreamRows) && p.in_dtype != MOEQ_ACT_F32 && !p.a_t && !p.b_t;
 }
 
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s) {
@@ -274,7 +283,7 @@ cudaError_t launch_product_stream(const Product &p, cudaStream_t s) {
         return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, EPI_STORE, float>(p, s)
                                            : launch_t<true, EPI_STORE, __nv_bfloat16>(p, s);
     }
-    return launch_t<false, EPI_GLU, __nv_bfloat16>(p, s);
+    return p.epi == EPI_GLU_BWD ? launch_t<false, EPI_GLU_BWD, __nv_bfloat16>(p, s) : launch_t<false, EPI_GLU, __nv_bfloat16>(p, s);
 }
 
 }  // namespace dense

@@ -452,7 +452,7 @@ MOEQ_API moeq_status moeq_glu(const moeq_glu_args *a, void *stream);
  *     dx = dg W_gate + du W_up,   dW_gate = dg^T x,   dW_up = du^T x
  * g and u are read from gu where it is given (as moeq_glu wrote it), else
  * computed again from x and w.  dg and du are rounded to dtype (they are the
- * operands of the products that follow); sums are f32, rounded once.  Outputs
+ * operands of the products that follow; up to 4 tokens may keep them f32); sums are f32, rounded once.  Outputs
  * are overwritten; dx NULL or both dw NULL leaves that gradient out (not
  * both).  Reads x, w, gu, dh; h is not read.  n_tokens == 0 sets dw to zero.
  * Errors: as moeq_glu. */

@@ -238,8 +238,10 @@ def test_glu(moeq, T, H, I, pad, off, dtype):
         check(got, ref, e + (ref.abs() + e) * EPS[dtype] * 1.001, what)
 
 
-def backward_refs(dh, x, wg, wu, g, u, eg, eu, dtype):
-    """Gradients in f64 and their bounds, from projections known to within eg, eu."""
+def backward_refs(dh, x, wg, wu, g, u, eg, eu, dtype, inner=None):
+    """Gradients in f64 and their bounds, from projections known to within eg, eu.
+    inner: the type that dg and du are held in, dtype without it."""
+    inner = EPS[inner or dtype]
     s = sigmoid(g)
     ds = s * (1 + g * (1 - s))               # |ds| <= 1.1, |d ds / dg| <= 0.5
     dh, x, wg, wu = dh.double(), x.double(), wg.double(), wu.double()
@@ -249,7 +251,7 @@ def backward_refs(dh, x, wg, wu, g, u, eg, eu, dtype):
     # evaluation in f32: ds is a sum of terms up to s (1 + |g|)
     bg = bg + MISC * (dh * u).abs() * s * (1 + g.abs())
     bu = bu + MISC * du.abs()
-    bg, bu = bg + (dg.abs() + bg) * EPS[dtype] * 1.001, bu + (du.abs() + bu) * EPS[dtype] * 1.001
+    bg, bu = bg + (dg.abs() + bg) * inner * 1.001, bu + (du.abs() + bu) * inner * 1.001
     gx, gt = gamma(2 * g.shape[1]), gamma(x.shape[0])
     out = []
     for ref, e, sm, gm in (
@@ -282,6 +284,37 @@ def test_glu_backward(moeq, T, H, I, pad, off, dtype):
         assert n1 is None and n2 is None and torch.equal(dx, got[0])
         n0, d1, d2 = moeq.glu_backward(dh, x, wg, wu, gu=kept, need_dx=False)
         assert n0 is None and torch.equal(d1, got[1]) and torch.equal(d2, got[2])
+
+
+FEW = [  # T, H, I, pad, off
+    (1, 1, 1, 0, 0), (1, 200, 69, 3, 0), (2, 64, 138, 0, 0), (3, 131, 70, 1, 1), (4, 1000, 513, 0, 0), (3, 40, 1030, 8, 8),
+    (4, 99, 317, 0, 3), (2, 576, 640, 0, 0), (4, 31, 9, 0, 0), (3, 15, 2100, 2, 0), (4, 64, 8000, 0, 0),
+]
+
+
+@pytest.mark.parametrize("T,H,I,pad,off", FEW)
+def test_glu_backward_of_few_tokens_rounds_once(moeq, T, H, I, pad, off):
+    """Up to 4 bf16 tokens, small weights: dg and du stay f32, so that the only rounding to
+    bf16 is the result's; empty rows of dh stay empty."""
+    torch = torch_mod()
+    x = mat(T, H, "bf16", 31, pad=pad, off=off)
+    wg, wu = mat(I, H, "bf16", 32, scale=1.3 / H ** 0.5, pad=pad), mat(I, H, "bf16", 33, scale=1.3 / H ** 0.5, off=off)
+    dh = mat(T, I, "bf16", 34, scale=0.1, pad=pad, off=off)
+    dh[T // 2] = 0
+    g, u, eg, eu = projections(x, wg, wu)
+    gu = torch.stack([g, u]).to(torch.bfloat16)
+    zero = torch.zeros_like(g)
+    for kept, pr in ((gu, (gu[0].double(), gu[1].double(), zero, zero)), (None, (g, u, eg, eu))):
+        outs = [framed(T, H, "bf16", pad, off), framed(I, H, "bf16", pad, off), framed(I, H, "bf16", pad)]
+        got = moeq.glu_backward(dh, x, wg, wu, gu=kept, dx=outs[0][0], dw_gate=outs[1][0], dw_up=outs[2][0])
+        refs = backward_refs(dh, x, wg, wu, *pr, "bf16", inner="f32")
+        for o, (ref, bound), what, fr in zip(got, refs, ("dx", "dwg", "dwu"), outs):
+            check(o, ref, bound, what + (" (kept)" if kept is not None else ""))
+            assert fr[1](), what
+        assert (got[0][T // 2] == 0).all()
+        dx, _, _ = moeq.glu_backward(dh, x, wg, wu, gu=kept, need_dw=False)
+        _, d1, d2 = moeq.glu_backward(dh, x, wg, wu, gu=kept, need_dx=False)
+        assert torch.equal(dx, got[0]) and torch.equal(d1, got[1]) and torch.equal(d2, got[2])
 
 
 def test_glu_gradients_against_differences(moeq):
