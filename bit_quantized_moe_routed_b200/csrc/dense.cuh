@@ -37,6 +37,7 @@ struct Product {
     void *out[2] = {nullptr, nullptr};       // per batch
     long long old[2] = {0, 0};
     void *keep[2] = {nullptr, nullptr};      // [M][N] planes, row stride kld
+    bool keep_f32 = false;                   // EPI_GLU_BWD of bf16: keep is f32 (dense_stream.cu alone writes it so)
     long long kld = 0;
     const void *dh = nullptr;                // [M][N], row stride dhld (EPI_GLU_BWD)
     long long dhld = 0;
@@ -139,9 +140,12 @@ cudaError_t launch_product_tc(const Product &p, cudaStream_t s);
 // as for launch_product_tc
 cudaError_t launch_gradients_tc(const Product *dx, const Product *dw, cudaStream_t s);
 // bf16 and int8, at most kStreamRows rows of A, any strides and alignment
-// (dense_stream.cu); EPI_GLU_BWD: keep is f32, at most kFewRows rows
-constexpr int kStreamRows = 16;
-bool stream_supported(const Product &p);
+// (dense_stream.cu); EPI_GLU_BWD: where keep is f32, at most kFewRows rows
+constexpr int kStreamRows = 16, kFewRows = 4;
+inline bool stream_supported(const Product &p) {
+    return (p.epi == EPI_GLU_BWD ? p.keep_f32 && p.M <= kFewRows : p.M <= kStreamRows) && p.in_dtype != MOEQ_ACT_F32 && !p.a_t &&
+           !p.b_t;
+}
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s);
 // bf16 and int8, K split over clusters; operands as for launch_product_tc
 // (dense_skinny.cu)
@@ -161,7 +165,6 @@ cudaError_t launch_pack(const Copy *c, int n, int es, cudaStream_t s);
 // bf16, at most kFewRows tokens, any strides and alignment: both gradients from
 // f32 gate gradients dg, du [T][dld] (dense_few.cu).  px, pw: dx and dW as for
 // launch_gradients_tc, either of them NULL; their A is not read.
-constexpr int kFewRows = 4;
 cudaError_t launch_few_gradients(const Product *px, const Product *pw, const float *dg, const float *du, long long dld,
                                  cudaStream_t s);
 cudaError_t launch_dgate_f32(const void *dh, long long dhld, const void *gu, float *dg, float *du, long long ld, int T, int N,

@@ -397,6 +397,7 @@ extern "C" moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream) {
         }
         p.keep[0] = dg;
         p.keep[1] = du;
+        p.keep_f32 = plan.few;   // the plan has sized them; the kernel follows
         p.kld = plan.dgu_ld;
         p.dh = a->dh;
         p.dhld = a->lddh;

@@ -361,6 +361,7 @@ long long skinny_ns(const Product &p, int sms) {
 
 cudaError_t launch_product_skinny(const Product &p, cudaStream_t s) {
     typedef __nv_bfloat16 B;
+    if (p.keep_f32) return cudaErrorInvalidValue;   // keep is written in out_dtype
     if (p.in_dtype == kI8) {
         if (p.epi == EPI_GLU)
             return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, false, false, EPI_GLU, float>(p, s)

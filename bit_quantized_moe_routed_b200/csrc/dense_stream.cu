@@ -271,11 +271,8 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
 
 }  // namespace
 
-bool stream_supported(const Product &p) {
-    return p.M <= (p.epi == EPI_GLU_BWD ? kFewRows : kStreamRows) && p.in_dtype != MOEQ_ACT_F32 && !p.a_t && !p.b_t;
-}
-
 cudaError_t launch_product_stream(const Product &p, cudaStream_t s) {
+    if (!stream_supported(p)) return cudaErrorInvalidValue;
     if (p.in_dtype == kI8) {
         if (p.epi == EPI_GLU)
             return p.out_dtype == MOEQ_ACT_F32 ? launch_t<true, EPI_GLU, float>(p, s)

@@ -559,6 +559,7 @@ long long tc_ns(const Product *ps, int n, int sms, int *bn) {
 
 cudaError_t launch_product_tc(const Product &p, cudaStream_t s) {
     typedef __nv_bfloat16 B;
+    if (p.keep_f32) return cudaErrorInvalidValue;   // keep is written in out_dtype
     if (p.in_dtype == kI8) {
         if (p.epi == EPI_GLU)
             return p.out_dtype == MOEQ_ACT_F32 ? launch_bn<true, false, EPI_GLU, float>(&p, 1, s)
