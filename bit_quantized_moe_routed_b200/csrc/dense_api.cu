@@ -196,15 +196,20 @@ bool glu_args_ok(const moeq_glu_args *a, bool backward) {
         if (a->dw[i] && !matrix_ok(a->dw[i], a->hidden, a->lddw[i], es)) return false;
     return true;
 }
-// The gradients of few tokens by dense_few.cu, or on the tensor cores.  Graphs of
-// back-to-back calls, us, dense_few.cu against tensor cores, 1 and 4 tokens:
-//   kept projections  512 x 517 7.1, 8.0 against 11.5, 11.3; 64 x 138 5.2, 6.2
-//     against 7.0, 7.0; 1024 x 1024 14.1, 15.1 against 13.2, 13.1
-//   recomputed  1024 x 1024 11.3, 13.6 against 16.4, 16.8; 1024 x 4096 22.7, 24.5
-//     against 42.5, 38.5; 4096 x 2048 20.3, 29.1 against 40.7, 40.7
-//   rows off 16 bytes, kept  77 x 69 6.6, 7.4 against 8.3, 8.5; 77 x 301 12.3, 12.8
-//     against 9.9, 10.0; 333 x 260 12.3, 12.7 against 10.2, 10.4.  There the
-//     limit is for accuracy: the smallest sums gain most from f32 dg and du.
+// The gradients of few tokens by dense_few.cu, or on the tensor cores.  Back-to-back
+// calls on weights that come from HBM, us, dense_few.cu against tensor cores:
+//   1 token, kept  1024 x 1024 14.3 against 13.3; 4096 x 1024 16.3, 19.6; 4096 x 2048
+//     19.7, 32.3; 4096 x 4096 34.9, 45.0; 4096 x 11008 92, 101 (2 tokens the same)
+//   1 token, recomputed  1024 x 1024 11.8, 16.2; 4096 x 2048 20.6, 40.5; 4096 x 4096
+//     45.0, 60.0; 4096 x 11008 125, 170
+//   4 tokens, kept  1024 x 1024 15.2, 13.4; 4096 x 2048 32.9, 32.4; 4096 x 4096 58.2, 45.4
+//   4 tokens, recomputed  4096 x 2048 29.2, 40.4; 4096 x 4096 60.7, 60.8; 4096 x 11008 186, 159
+// so at any size for 2 tokens, up to 2^23 for 4, whether the projections are kept or not.
+//   rows off 16 bytes, 1 token  kept 77 x 69 6.8, 8.5; 99 x 130 11.7, 8.6; 255 x 255 13.4,
+//     9.5; 576 x 640 20.7, 15.0; recomputed 77 x 69 9.8, 12.6; 255 x 255 16.4, 14.4; 1000 x
+//     517 26.0, 17.3; 4096 x 2048 111, 66
+// There the elements go one by one and the time alone would end it at 2^13; up to 2^16 it
+// costs at most 6 us, which f32 dg and du are taken to be worth.
 // Only what both gradients need decides, so that asking for one changes no bits.
 bool few_tokens(const moeq_glu_args *a) {
     if (a->dtype != MOEQ_ACT_BF16 || a->n_tokens > kFewRows) return false;
@@ -212,7 +217,7 @@ bool few_tokens(const moeq_glu_args *a) {
     const bool aligned = rows16(a->x, a->ldx) && rows16(a->w[0], a->ldw[0]) && rows16(a->w[1], a->ldw[1]);
     const long long size = (long long)a->hidden * a->inter;
     if (!aligned) return size <= 1 << 16;
-    return a->gu ? size <= 1 << 19 : size * a->n_tokens <= 1 << 25;
+    return a->n_tokens <= 2 || size <= 1 << 23;
 }
 
 Plan plan_glu(const moeq_glu_args *a, bool backward) {

@@ -29,8 +29,8 @@ def workspace_of(moeq, dh, x, wg, wu, gu, outs):
     return buf[guard:guard + n], untouched
 
 
-# T, H, I, pad, off: rows on 16 bytes and off them; the sizes lie on both sides of hidden * inter = 2^16 and 2^19 and of
-# T * hidden * inter = 2^25
+# T, H, I, pad, off: rows on 16 bytes and off them; the sizes lie on both sides of hidden * inter = 2^16, 2^19 and
+# 2^23 and of T * hidden * inter = 2^25
 LIMITS = [
     (1, 4096, 11008, 0, 0), (4, 4096, 4096, 0, 0), (1, 333, 260, 1, 0), (4, 1000, 517, 3, 0), (2, 1000, 517, 3, 1),
     (2, 256, 256, 3, 0), (2, 257, 256, 3, 0), (1, 301, 217, 0, 5), (3, 1024, 512, 0, 0), (3, 1024, 520, 0, 0),
@@ -62,3 +62,21 @@ def test_gradients_on_both_sides_of_the_limits(moeq, T, H, I, pad, off):
         dx, _, _ = moeq.glu_backward(dh, x, wg, wu, gu=kept, need_dw=False)
         _, d1, d2 = moeq.glu_backward(dh, x, wg, wu, gu=kept, need_dx=False)
         assert torch.equal(dx, got[0]) and torch.equal(d1, got[1]) and torch.equal(d2, got[2])
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 1024, 1024), (1, 4096, 11008), (2, 4096, 4096), (2, 2056, 5504), (3, 1000, 4000),
+                                   (4, 4096, 2048)])
+def test_kept_and_recomputed_projections_round_once(moeq, T, H, I):
+    """Rows on 16 bytes, 1 and 2 tokens at any size, 3 and 4 up to 2^23 weights: dg and du stay f32
+    with the projections kept as well as without them."""
+    torch = torch_mod()
+    x, dh = mat(T, H, "bf16", 111), mat(T, I, "bf16", 114, scale=0.1)
+    wg, wu = mat(I, H, "bf16", 112, scale=1.3 / H ** 0.5), mat(I, H, "bf16", 113, scale=1.3 / H ** 0.5)
+    g, u, eg, eu = projections(x, wg, wu)
+    gu = torch.stack([g, u]).to(torch.bfloat16)
+    zero = torch.zeros_like(g)
+    for kept, pr in ((gu, (gu[0].double(), gu[1].double(), zero, zero)), (None, (g, u, eg, eu))):
+        got = moeq.glu_backward(dh, x, wg, wu, gu=kept)
+        refs = backward_refs(dh, x, wg, wu, *pr, "bf16", inner="f32")
+        for o, (ref, bound), name in zip(got, refs, ("dx", "dwg", "dwu")):
+            check(o, ref, bound, name + (" (kept)" if kept is not None else ""))
