@@ -191,7 +191,7 @@ cudaError_t launch(const void *x, int rows, int cols, long long ldx, int8_t *q, 
     const bool vec = !((uintptr_t)x & 15u) && !((ldx * sizeof(T)) & 15u) && !((uintptr_t)q & 7u) && !(ldq & 7);
     auto run = [&](auto tpr) {
         constexpr int kTpr = decltype(tpr)::value;
-        const int per = kQThreads / kTpr, grid = (rows + per - 1) / per;
+        const long long per = kQThreads / kTpr, grid = (rows + per - 1) / per;   // rows reach 2^31 - 1
         return dense::launch_pdl(vec ? quant_i8_kernel<T, kTpr, true> : quant_i8_kernel<T, kTpr, false>, dim3((unsigned)grid),
                                  kQThreads, 0, 0, s, xt, ldx, rows, cols, q, ldq, scale);
     };

@@ -1,8 +1,11 @@
-"""The backward pass of the gated block on the host: the entry points over
-launchers that only note what their kernels write and read (host/dense_plan.cpp).
+"""Decisions of the dense operators on the host.
+
+The backward pass of the gated block: the entry points over launchers that only
+note what their kernels write and read (host/dense_plan.cpp).
 Every step stays inside the workspace that the query names, no part lies on
 another, and each kernel reads the gate gradients in the type they were
 written in, on both sides of every limit between kernels."""
+import glob
 import itertools
 import os
 import subprocess
@@ -12,17 +15,17 @@ import pytest
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 
-@pytest.fixture(scope="module")
-def plan(tmp_path_factory):
+def program(tmp, name, objects, flags=()):
+    """A host program of one source and objects of the library: f(cases) -> lines, a case's numbers on a line."""
     from bit_quantized_moe_routed_b200 import build
     build.build()
-    out = str(tmp_path_factory.mktemp("plan") / "dense_plan")
-    r = subprocess.run([build.NVCC, *build.ARCH, "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, "-x", "cu",
-                        os.path.join(HERE, "host", "dense_plan.cpp"), "-o", out + ".o", "-c"], capture_output=True, text=True)
-    assert r.returncode == 0, r.stderr
-    r = subprocess.run([build.NVCC, *build.ARCH, out + ".o", os.path.join(build.BUILD, "dense_api.o"), "-o", out],
-                       capture_output=True, text=True)
-    assert r.returncode == 0, r.stderr
+    out = str(tmp / name)
+    objs = [o for pattern in objects for o in glob.glob(os.path.join(build.BUILD, pattern))]
+    for cmd in ([*build.ARCH, "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, "-x", "cu",
+                 os.path.join(HERE, "host", name + ".cpp"), "-c", "-o", out + ".o"],
+                [*build.ARCH, *flags, out + ".o", *objs, "-o", out]):
+        r = subprocess.run([build.NVCC, *cmd], capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
 
     def run(cases):
         text = "".join(" ".join(str(int(v)) for v in c) + "\n" for c in cases)
@@ -30,6 +33,11 @@ def plan(tmp_path_factory):
         assert r.returncode == 0, r.stderr
         return r.stdout.split("\n")[:-1]
     return run
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    return program(tmp_path_factory.mktemp("plan"), "dense_plan", ["dense_api.o"])
 
 
 SIZES = [(1, 1), (64, 138), (256, 256), (257, 256), (77, 301), (333, 260), (1000, 517), (1024, 512), (1024, 520),
@@ -46,3 +54,12 @@ def test_backward_stays_in_its_workspace(plan, T):
     assert len(got) == len(cases)
     bad = [(c, g) for c, g in zip(cases, got) if g != "ok"]
     assert not bad, f"{len(bad)} of {len(cases)}, the first: {bad[:3]}"
+
+
+def test_quantiser_grid_covers_its_rows(tmp_path):
+    """Up to the 2^31 - 1 rows that the call takes: a thread group for each row, none lost to 32-bit sums."""
+    run = program(tmp_path, "quant_grid", ["*.o"], ["-Xlinker", "--wrap=cudaLaunchKernelExC"])
+    cases = [(r, c) for r in (1, 7, 8, 9, 2**31 - 9, 2**31 - 8, 2**31 - 7, 2**31 - 1) for c in (1, 1024, 1025, 4096, 4097)]
+    for (rows, cols), line in zip(cases, run(cases), strict=True):
+        per = 8 if cols <= 1024 else (2 if cols <= 4096 else 1)
+        assert line == f"{-(-rows // per)} 1 1 256", (rows, cols, line)
