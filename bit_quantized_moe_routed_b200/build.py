@@ -5,16 +5,21 @@
 to date), then they link into ``bit_quantized_moe_routed_b200/libmoeq.so``.
 No GPU is needed: nvcc cross-compiles.  ``csrc/torch_calls.cpp`` (the torch
 side of the dense operators' Python calls) compiles with g++ against the
-installed torch into ``_torch_calls.so`` beside it.
+installed torch into ``_torch_calls.so`` beside it, again where that torch or
+Python is another one; without torch or the headers it is left out, and the
+library and the rest of the binding build and load as they do with it.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import hashlib
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +30,7 @@ SO = os.path.join(PKG, "libmoeq.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 CALLS_SO = os.path.join(PKG, "_torch_calls.so")
+CALLS_STAMP = os.path.join(BUILD, "torch_calls.stamp")   # what CALLS_SO was built against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -52,19 +58,38 @@ def _compile(src: str, force: bool, verbose: bool, extra: list) -> str:
     return obj
 
 
-def _build_calls(force: bool, verbose: bool) -> None:
-    deps = (CALLS_SRC, os.path.join(INCLUDE, "moeq.h"))
-    if (not force and os.path.exists(CALLS_SO)
-            and os.path.getmtime(CALLS_SO) >= max(os.path.getmtime(f) for f in deps)):
-        return
-    import sysconfig
+def _torch_root():
+    """The installed torch's directory (without importing it), or None."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        return None
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
+
+def _build_calls(force: bool, verbose: bool) -> None:
+    root = _torch_root()
+    python_inc = sysconfig.get_paths()["include"]
+    needed = [os.path.join(root, "include", "ATen", "ATen.h")] if root else []
+    needed.append(os.path.join(python_inc, "Python.h"))
+    missing = [h for h in needed if not os.path.exists(h)]
+    if not root or missing:
+        print(f"{os.path.basename(CALLS_SO)} is not built (the dense operators' Python calls need it): "
+              f"{'torch is not installed' if not root else 'no ' + ', '.join(missing)}", file=sys.stderr)
+        return
+    with open(os.path.join(root, "version.py"), "rb") as f:   # version, CUDA version and commit
+        key = hashlib.sha256(f.read() + f"{root}\n{sys.version}\n".encode()).hexdigest()
+    deps = (CALLS_SRC, os.path.join(INCLUDE, "moeq.h"))
+    if (not force and os.path.exists(CALLS_SO) and os.path.exists(CALLS_STAMP)
+            and os.path.getmtime(CALLS_SO) >= max(os.path.getmtime(f) for f in deps)):
+        with open(CALLS_STAMP) as f:
+            if f.read().strip() == key:
+                return
     import torch
-    root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = CALLS_SO + f".tmp{os.getpid()}"
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+           os.path.join(cuda, "include"), python_inc, INCLUDE]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DUSE_CUDA",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for d in inc:
@@ -77,6 +102,9 @@ def _build_calls(force: bool, verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS_SO)
+    with open(CALLS_STAMP + f".tmp{os.getpid()}", "w") as f:
+        f.write(key + "\n")
+    os.replace(f.name, CALLS_STAMP)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

@@ -16,11 +16,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 def program(tmp, name, objects, flags=()):
-    """A host program of one source and objects of the library: f(cases) -> lines, a case's numbers on a line."""
+    """A host program of one source and the library's objects of these sources (all of them for none): f(cases) -> lines, a case's numbers on a line."""
     from bit_quantized_moe_routed_b200 import build
     build.build()
     out = str(tmp / name)
-    objs = [o for pattern in objects for o in glob.glob(os.path.join(build.BUILD, pattern))]
+    srcs = objects or [os.path.basename(f)[:-3] for f in glob.glob(os.path.join(build.CSRC, "*.cu"))]
+    objs = [os.path.join(build.BUILD, f + ".o") for f in srcs]
     for cmd in ([*build.ARCH, "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, "-x", "cu",
                  os.path.join(HERE, "host", name + ".cpp"), "-c", "-o", out + ".o"],
                 [*build.ARCH, *flags, out + ".o", *objs, "-o", out]):
@@ -37,7 +38,7 @@ def program(tmp, name, objects, flags=()):
 
 @pytest.fixture(scope="module")
 def plan(tmp_path_factory):
-    return program(tmp_path_factory.mktemp("plan"), "dense_plan", ["dense_api.o"])
+    return program(tmp_path_factory.mktemp("plan"), "dense_plan", ["dense_api"])
 
 
 SIZES = [(1, 1), (64, 138), (256, 256), (257, 256), (77, 301), (333, 260), (1000, 517), (1024, 512), (1024, 520),
@@ -58,7 +59,7 @@ def test_backward_stays_in_its_workspace(plan, T):
 
 def test_quantiser_grid_covers_its_rows(tmp_path):
     """Up to the 2^31 - 1 rows that the call takes: a thread group for each row, none lost to 32-bit sums."""
-    run = program(tmp_path, "quant_grid", ["*.o"], ["-Xlinker", "--wrap=cudaLaunchKernelExC"])
+    run = program(tmp_path, "quant_grid", [], ["-Xlinker", "--wrap=cudaLaunchKernelExC"])
     cases = [(r, c) for r in (1, 7, 8, 9, 2**31 - 9, 2**31 - 8, 2**31 - 7, 2**31 - 1) for c in (1, 1024, 1025, 4096, 4097)]
     for (rows, cols), line in zip(cases, run(cases), strict=True):
         per = 8 if cols <= 1024 else (2 if cols <= 4096 else 1)
