@@ -47,19 +47,26 @@ struct Product {
 };
 constexpr int kI8 = 100;
 
-// The sigmoid 1 / (1 + e^-g).  For bf16 results the exponential and the
-// divide are the hardware's approximations: off by at most 2 ulp and by
-// |g| 2^-23 (the rounding of g log2 e in the exponent), below 2^-16 wherever
-// e^-g stays in f32, against the 2^-9 of the rounding that follows; e^-g
-// beyond 2^126 (g < -87.3) gives 0 for a value below 2^-126.  The IEEE divide
-// and expf made the gated epilogue 10 us longer at 2048 x 4096 x 2048.
+// sigmoid(g) = 1 / (1 + e^-g) and silu(g) = g sigmoid(g), from z = e^-|g|, which
+// does not overflow: for g < 0 they are z / (1 + z) and g z / (1 + z), so that
+// they fall off gradually (silu(-90) = -7e-38) instead of becoming 0 where e^-g
+// leaves f32.  For bf16 results the exponential and the divide (by 1 to 2) are
+// the hardware's approximations: off by at most 2 ulp each and by |g| 2^-23 (the
+// rounding of g log2 e in the exponent), below 2^-16 as long as z is normal,
+// against the 2^-9 of the rounding that follows.  The IEEE divide and expf made
+// the gated epilogue 10 us longer at 2048 x 4096 x 2048.
+template <bool FAST>
+__device__ __forceinline__ float over_1_plus_z(float g, float at_plus, float at_minus) {   // (g < 0 ? at_minus z : at_plus) / (1 + z)
+    const float z = FAST ? __expf(-fabsf(g)) : expf(-fabsf(g)), n = g < 0.f ? at_minus * z : at_plus;
+    return FAST ? __fdividef(n, 1.0f + z) : n / (1.0f + z);
+}
 template <bool FAST>
 __device__ __forceinline__ float sigmoid_f32(float g) {
-    return FAST ? __fdividef(1.0f, 1.0f + __expf(-g)) : 1.0f / (1.0f + expf(-g));
+    return over_1_plus_z<FAST>(g, 1.0f, 1.0f);
 }
 template <bool FAST>
 __device__ __forceinline__ float silu(float g) {
-    return FAST ? __fdividef(g, 1.0f + __expf(-g)) : silu_f32(g);
+    return over_1_plus_z<FAST>(g, g, g);
 }
 // dg and du for the gradient dh of silu(g) u
 template <bool FAST>

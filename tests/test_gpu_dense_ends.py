@@ -20,3 +20,40 @@ def test_quant_i8_of_the_most_rows(moeq):
         assert torch.equal(q[i:i + piece, 0], (127 * v.sign()).to(torch.int8))
         # f64 quotients of f32 values round to the f32 quotient; a / 127 in f32 torch takes as a product with 1 / 127
         assert torch.equal(scale[i:i + piece], (v.double().abs() / 127).float())
+
+
+@pytest.mark.parametrize("T", [3, 16, 40, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_silu_falls_off_gradually(moeq, dtype, T):
+    """Gates from -80 to -104, where e^-g leaves f32 (at -88.7) and silu(g) the normal range (at -92), through every
+    kernel of the block (few tokens, cluster, tiles, f32), forward and backward.  With z = e^g the values are g z and
+    z (1 + g) to within z^2.  z is off by |g| 2^-23 + 2 ulp < 1.3e-5 and in the subnormal range by a few of its steps
+    of 2^-149; the divide and the products add 2 + 3 ulp; then the result's own rounding, whose steps end at 2^-133 for
+    bf16, as those of the gate gradients do in both types (f32: their bf16 parts)."""
+    torch = torch_mod()
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    half, step = {"bf16": (2.0 ** -8, 2.0 ** -133), "f32": (2.0 ** -24, 2.0 ** -149)}[dtype]
+    H, I = 64, 48
+    gates = -80 - 0.5 * torch.arange(I, device="cuda", dtype=torch.float32)      # exact in bf16
+    x, wg, wu = (torch.zeros(s, device="cuda", dtype=dt) for s in ((T, H), (I, H), (I, H)))
+    x[:, 0], x[:, 1] = 1, 1
+    wg[:, 0], wu[:, 1] = gates.to(dt), 1
+    h, gu = moeq.glu(x, wg, wu, save=True)
+    g = gates.double()
+    s = torch.exp(g) / (1 + torch.exp(g))
+    assert torch.equal(gu[0].double(), g.expand(T, I)) and (gu[1] == 1).all()
+
+    def close(got, want, what, step=step):
+        rel = 1.3e-5 + 16 * 2.0 ** -23
+        bound = want.abs() * (rel + half) + 8 * g.abs() * 2.0 ** -149 + step
+        bad = (got.double() - want).abs() > bound
+        assert not bad.any(), f"{what}: {got[bad][:4].tolist()}, not {want.expand_as(got)[bad][:4].tolist()}"
+    close(h, g * s, "h")
+    # rows of dh with one token each: dW_up = silu(g) at x's 1, dW_gate = s (1 + g (1 - s)) there
+    dh = torch.zeros((T, I), device="cuda", dtype=dt)
+    dh[T // 2] = 1
+    for kept in (gu, None):
+        _, dwg, dwu = moeq.glu_backward(dh, x, wg, wu, gu=kept, need_dx=False)
+        # dg and du may be rounded to the type once more on the way
+        close(dwg[:, 0], s * (1 + g * (1 - s)), "dwg", 2.0 ** -132)
+        close(dwu[:, 1], g * s, "dwu", 2.0 ** -132)
