@@ -64,3 +64,27 @@ def test_quantiser_grid_covers_its_rows(tmp_path):
     for (rows, cols), line in zip(cases, run(cases), strict=True):
         per = 8 if cols <= 1024 else (2 if cols <= 4096 else 1)
         assert line == f"{-(-rows // per)} 1 1 256", (rows, cols, line)
+
+
+@pytest.mark.parametrize("T,H,I,off,dtype,kept,want", [
+    # bf16 gate gradients [2][T][I padded to 64]: in f32 for few tokens
+    (1, 4096, 11008, 0, 1, 0, 2 * 11008 * 4), (1, 4096, 11008, 0, 1, 1, 2 * 11008 * 4),
+    (4, 4096, 2048, 0, 1, 0, 2 * 4 * 2048 * 4), (4, 4096, 2056, 0, 1, 0, 2 * 4 * 2112 * 2),
+    (3, 4096, 2056, 0, 1, 1, 2 * 3 * 2112 * 2), (5, 4096, 4096, 0, 1, 0, 2 * 5 * 4096 * 2),
+    (2, 256, 256, 3, 1, 0, 2 * 2 * 256 * 4),
+    # rows off 16 bytes: and x [T] and both W [I] in rows of 128 bytes' multiples (H = 257: 640 bytes)
+    (2, 257, 256, 3, 1, 0, 2 * 640 + 2 * 256 * 640 + 2 * 2 * 256 * 2),
+    (300, 257, 256, 3, 1, 1, 300 * 640 + 2 * 256 * 640 + 2 * 300 * 256 * 2),
+    # f32: three planes each of x, both W, dg and du, rows padded to 64
+    (4, 64, 32, 0, 0, 0, 3 * 4 * 64 * 2 + 2 * 3 * 32 * 64 * 2 + 2 * 3 * 4 * 64 * 2),
+    (4, 64, 32, 3, 0, 1, 3 * 4 * 64 * 2 + 2 * 3 * 32 * 64 * 2 + 2 * 3 * 4 * 64 * 2),
+])
+def test_backward_workspace_to_the_byte(T, H, I, off, dtype, kept, want):
+    from bit_quantized_moe_routed_b200 import build
+    build.build()
+    from bit_quantized_moe_routed_b200 import moeq
+    a = [k << 40 for k in range(1, 9)]
+    ldh, ldi = H + off, I + off
+    args = moeq.GLU_ARGS.pack(T, H, I, dtype, a[0], ldh, a[1], a[2], ldh, ldh, a[3] if kept else 0, 0, 0, a[4], ldi, a[5], ldh,
+                              a[6], a[7], ldh, ldh, 0, 0)
+    assert moeq.lib().moeq_glu_workspace(args, 1) == want
