@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
     } else if (warp >= 4) {
         const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         for (int q = 0; q < chunks; ++q) {
-            if (!mbar_wait_abort(&main_full[q & 1], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
+            if (!warp_wait_abort(&main_full[q & 1], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
             tc_fence_after();
 #pragma unroll
             for (int h = 0; h < kNT / 32; ++h) {

@@ -302,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         for (TileWalk at(p, pair, pairs); at.next(); ++q) {
             const TcWork &w = p.w[at.work];
             const int b = q & 1;
-            if (!mbar_wait_abort(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
+            if (!warp_wait_abort(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
             tc_fence_after();
             const long long m0 = (long long)at.m * 2 * kTileM + rank * kTileM + quad * 32, n0 = (long long)at.n * kOutN;
             const int rows = (int)min(32LL, w.M - m0);

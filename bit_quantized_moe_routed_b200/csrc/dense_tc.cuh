@@ -66,6 +66,12 @@ __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, vol
     return true;
 }
 
+// mbar_wait_abort by a whole warp: it gives up as one, as the tensor memory
+// loads that follow are instructions of the warp.
+__device__ __forceinline__ bool warp_wait_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag, long long max_cycles) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_abort(bar, parity, abort_flag, max_cycles));
+}
+
 // Shared-memory descriptor of an operand whose 128-byte rows run along M or
 // N (stored [K][M]): 128-byte swizzle, blocks of 64 elements `lbo` bytes
 // apart, groups of 8 K-rows 1024 bytes apart.
