@@ -152,10 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < kNT; ++i) tot[i] = 0.f;
 
+    int issued = 0;   // loads, by thread 0
     if (warp == 0 && lane == 0) {
-        int c = 0;
-        for (; c < kbs; ++c) {
-            const int s = c % kStages, kb = kb0 + c, seg = w.nseg > 1 && kb >= w.kblocks, k0 = (seg ? kb - w.kblocks : kb) * 64;
+        for (; issued < kbs; ++issued) {
+            const int c = issued, s = c % kStages, kb = kb0 + c, seg = w.nseg > 1 && kb >= w.kblocks, k0 = (seg ? kb - w.kblocks : kb) * 64;
             if (c >= kStages && !wait_cluster(&empty[s], (uint32_t)((c / kStages - 1) & 1), &abort_flag)) break;
             uint8_t *sa = smem + s * kStage, *sb = sa + kABytes;
             mbar_arrive_expect_tx(&full[s], kStage);
@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
             if (b_mn) tma_load_3d(sb, mb, m0, k0, 0, &full[s]);
             else tma_load_3d(sb, mb, k0, m0, 0, &full[s]);
         }
-        if (abort_flag) drain_stages(full, kStages, c);
     } else if (warp == 1 && lane == 0) {
         const uint32_t id = b_mn ? idesc_dense<false>(kT, kNT, A_MN, true) : idesc_dense<false>(kT, kNT, A_MN, false);
         const uint64_t bstep = b_mn ? 2048 >> 4 : 32 >> 4;
@@ -225,6 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
     const bool ok = mbar_wait_abort(&done, 0, &abort_flag, kWaitCycles);
     if (!ok) mbar_wait_bounded(&done, 0, kDrainCycles);
     __syncthreads();   // every load has been consumed: the ring is free
+    if (abort_flag) {   // or not: copies that nobody waited for land first. Every wait is behind: the same for all
+        if (threadIdx.x == 0) drain_stages(full, kStages, issued);
+        __syncthreads();
+    }
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);   // [row of B][row of A]
     if (warp >= 4) {

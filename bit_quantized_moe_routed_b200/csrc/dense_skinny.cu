@@ -175,7 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
             if (!wait_cluster(&empty[issued % S], (uint32_t)((issued / S - 1) & 1), &abort_flag)) break;
             load(issued);
         }
-        if (abort_flag) drain_stages(full, S, issued);
     } else if (warp == 1 && lane == 0) {
         const uint32_t id = idesc_dense<I8>(kT, p.nt, A_MN, B_MN);
         for (int c = 0; c < kb1 - kb0; ++c) {
@@ -199,6 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
     const bool ok = mbar_wait_abort(&done, 0, &abort_flag, kWaitCycles);
     if (!ok) mbar_wait_bounded(&done, 0, kDrainCycles);
     __syncthreads();
+    if (abort_flag) {   // every wait is behind: the same for all. Copies that nobody waited for land first
+        if (threadIdx.x == 0) drain_stages(full, S, issued);
+        __syncthreads();
+    }
     tc_fence_after();
     uint32_t *part = reinterpret_cast<uint32_t *>(smem);
     if (warp >= 4) {

@@ -251,13 +251,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 boxes(at, w, kb, [&](int off, const CUtensorMap *map, int x, int y) { tma_load_pair(st + off, map, x, y, bar); });
             }
         }
-        // the ring's last stages: consumed before this SM's shared memory goes away
-        for (int i = c > S ? c - S : 0; i < c; ++i) {
-            const long long t0 = clock64();
-            while (!test_wait_cluster(&empty[i % S], (uint32_t)((i / S) & 1)) &&
-                   clock64() - t0 < (ok ? kWaitCycles : kDrainCycles)) {
+        // the ring's last stages: consumed before this SM's shared memory goes away,
+        // or, once a role has given up, landed long since (this SM cannot wait for
+        // the pair's barrier)
+        const long long t0 = clock64(), drain = ok ? kWaitCycles : kDrainCycles;
+        for (int i = c > S ? c - S : 0; i < c; ++i)
+            while (!test_wait_cluster(&empty[i % S], (uint32_t)((i / S) & 1)) && clock64() - t0 < drain) {
             }
-        }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- MMAs of the pair
         int c = 0, q = 0;
@@ -287,11 +287,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             }
             if (ok) commit_pair(&acc_full[b]);
         }
-        if (abort_flag) {   // MMAs in flight end before the tensor memory goes away
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done))
-                         : "memory");
-            mbar_wait_bounded(&done, 0, kDrainCycles);
-        }
+        // MMAs in flight end before the tensor memory goes away, whichever role gives up and when
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done))
+                     : "memory");
+        mbar_wait_bounded(&done, 0, kDrainCycles);
     } else if (warp >= 4) {
         // ---- epilogue: warp w reads lanes 32 (w % 4).., columns by halves
         const int e = warp - 4, quad = e & 3, half = e >> 2;
