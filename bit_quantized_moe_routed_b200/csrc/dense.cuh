@@ -203,6 +203,8 @@ cudaError_t launch_dgate_planes(const float *dh, long long dhld, const float *gu
 // SMs of the current device; address of its status word (dense_tc.cu).
 cudaError_t sm_count(int *n);
 cudaError_t status_word(uint32_t **p);
+// Read the limit of the kernels' waits from the environment again (dense_tc.cu).
+void read_wait_cycles();
 // dg, du (row stride ld) = the gradients of the kept projections gu [2][M][N], bf16
 cudaError_t launch_glu_dgate(const void *dh, long long dhld, const void *gu, void *dg, void *du, long long ld,
                              long long M, long long N, cudaStream_t s);

@@ -455,6 +455,7 @@ extern "C" moeq_status moeq_dense_status(int32_t clear) {
     uint32_t *at = nullptr, w = 0;
     if (status_word(&at) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return MOEQ_ERR_CUDA;
     if (cudaMemcpy(&w, at, sizeof(w), cudaMemcpyDeviceToHost) != cudaSuccess) return MOEQ_ERR_CUDA;
-    if (clear && w && cudaMemset(at, 0, sizeof(w)) != cudaSuccess) return MOEQ_ERR_CUDA;
+    if (clear) read_wait_cycles();
+    if (clear && w && (cudaMemset(at, 0, sizeof(w)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)) return MOEQ_ERR_CUDA;
     return w ? MOEQ_ERR_TIMEOUT : MOEQ_OK;
 }

@@ -57,6 +57,7 @@ struct PlanesArgs {
     long long kld, kplane;
     const float *dh;
     long long dhld;
+    long long wait_cycles;
     uint32_t *status;
 };
 
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
     if (warp == 0 && lane == 0) {
         for (; issued < kbs; ++issued) {
             const int c = issued, s = c % kStages, kb = kb0 + c, seg = w.nseg > 1 && kb >= w.kblocks, k0 = (seg ? kb - w.kblocks : kb) * 64;
-            if (c >= kStages && !wait_cluster(&empty[s], (uint32_t)((c / kStages - 1) & 1), &abort_flag)) break;
+            if (c >= kStages && !wait_cluster(&empty[s], (uint32_t)((c / kStages - 1) & 1), &abort_flag, p.wait_cycles)) break;
             uint8_t *sa = smem + s * kStage, *sb = sa + kABytes;
             mbar_arrive_expect_tx(&full[s], kStage);
             if (A_MN) {   // [64 columns][plane][64 rows of K]
@@ -179,8 +180,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
         bool ok = true;
         for (int c = 0; ok && c < kbs; ++c) {
             const int s = c % kStages, q = c / kChunk, buf = q & 1;
-            if (c % kChunk == 0 && q >= 2 && !wait_cluster(&main_empty[buf], (uint32_t)(((q >> 1) - 1) & 1), &abort_flag)) break;
-            if (!wait_cluster(&full[s], (uint32_t)((c / kStages) & 1), &abort_flag)) break;
+            if (c % kChunk == 0 && q >= 2 &&
+                !wait_cluster(&main_empty[buf], (uint32_t)(((q >> 1) - 1) & 1), &abort_flag, p.wait_cycles))
+                break;
+            if (!wait_cluster(&full[s], (uint32_t)((c / kStages) & 1), &abort_flag, p.wait_cycles)) break;
             tc_fence_after();
             const uint8_t *sa = smem + s * kStage, *sb = sa + kABytes;
             uint64_t da[3], db[3];
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
     } else if (warp >= 4) {
         const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         for (int q = 0; q < chunks; ++q) {
-            if (!warp_wait_abort(&main_full[q & 1], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
+            if (!warp_wait_abort(&main_full[q & 1], (uint32_t)((q >> 1) & 1), &abort_flag, p.wait_cycles)) break;
             tc_fence_after();
 #pragma unroll
             for (int h = 0; h < kNT / 32; ++h) {
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_planes_kernel(const __gri
         }
     }
     __syncwarp();
-    const bool ok = mbar_wait_abort(&done, 0, &abort_flag, kWaitCycles);
+    const bool ok = mbar_wait_abort(&done, 0, &abort_flag, p.wait_cycles);
     if (!ok) mbar_wait_bounded(&done, 0, kDrainCycles);
     __syncthreads();   // every load has been consumed: the ring is free
     if (abort_flag) {   // or not: copies that nobody waited for land first. Every wait is behind: the same for all
@@ -307,6 +310,7 @@ cudaError_t launch_t(const PlanesProduct *ps, int nwork, cudaStream_t s) {
     int sms = 0;
     cudaError_t e = status_word(&a.status);
     if (e == cudaSuccess) e = sm_count(&sms);
+    a.wait_cycles = wait_cycles();
     a.size = 1;
     for (int j = 0; j < nwork && e == cudaSuccess; ++j) {
         const PlanesProduct &p = ps[j];

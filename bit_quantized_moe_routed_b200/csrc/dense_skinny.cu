@@ -47,6 +47,7 @@ struct SkinnyArgs {
     long long kld;
     const void *dh;
     long long dhld;
+    long long wait_cycles;
     uint32_t *status;
 };
 
@@ -172,14 +173,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
 
     if (warp == 0 && lane == 0) {
         while (issued < kb1 - kb0) {
-            if (!wait_cluster(&empty[issued % S], (uint32_t)((issued / S - 1) & 1), &abort_flag)) break;
+            if (!wait_cluster(&empty[issued % S], (uint32_t)((issued / S - 1) & 1), &abort_flag, p.wait_cycles)) break;
             load(issued);
         }
     } else if (warp == 1 && lane == 0) {
         const uint32_t id = idesc_dense<I8>(kT, p.nt, A_MN, B_MN);
         for (int c = 0; c < kb1 - kb0; ++c) {
             const int s = c % S;
-            if (!wait_cluster(&full[s], (uint32_t)((c / S) & 1), &abort_flag)) break;
+            if (!wait_cluster(&full[s], (uint32_t)((c / S) & 1), &abort_flag, p.wait_cycles)) break;
             tc_fence_after();
             const uint8_t *st = smem + s * stage_bytes;
             const uint64_t da = A_MN ? desc_mn_sw128(st, 8192) : desc_sw128(st);
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_skinny_kernel(const __gri
     __syncwarp();   // the other lanes of the issuing warps do not poll beside them
     // ---- this CTA's sums into its shared memory, [token][row]: the ring is
     // free once every MMA has completed (every load has been consumed by then)
-    const bool ok = mbar_wait_abort(&done, 0, &abort_flag, kWaitCycles);
+    const bool ok = mbar_wait_abort(&done, 0, &abort_flag, p.wait_cycles);
     if (!ok) mbar_wait_bounded(&done, 0, kDrainCycles);
     __syncthreads();
     if (abort_flag) {   // every wait is behind: the same for all. Copies that nobody waited for land first
@@ -316,6 +317,7 @@ cudaError_t launch_t(const Product &p, cudaStream_t s) {
         e = B_MN ? make_map(&a.b[i], p.a[i], p.K, p.M, p.ald, es, 64) : make_map(&a.b[i], p.a[i], p.M, p.K, p.ald, es, a.nt);
     if (e == cudaSuccess) e = status_word(&a.status);
     if (e != cudaSuccess) return e;
+    a.wait_cycles = wait_cycles();
     a.a_scale = p.a_scale;
     for (int i = 0; i < 2; ++i) {
         a.b_scale[i] = p.b_scale[i];

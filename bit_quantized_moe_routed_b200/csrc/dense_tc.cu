@@ -26,6 +26,7 @@
 // status word.
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 #include <mutex>
 #include <utility>
 
@@ -69,6 +70,7 @@ struct TcArgs {
     const void *dh;
     long long dhld;
     bool vec_keep, vec_dh;
+    long long wait_cycles;
     uint32_t *status;
 };
 
@@ -241,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             const int kb_total = w.kb_total();
             for (int kb = 0; kb < kb_total; ++kb, ++c) {
                 const int s = c % S;
-                if (c >= S && !wait_cluster(&empty[s], (uint32_t)((c / S - 1) & 1), &abort_flag)) {
+                if (c >= S && !wait_cluster(&empty[s], (uint32_t)((c / S - 1) & 1), &abort_flag, p.wait_cycles)) {
                     ok = false;
                     break;
                 }
@@ -254,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         // the ring's last stages: consumed before this SM's shared memory goes away,
         // or, once a role has given up, landed long since (this SM cannot wait for
         // the pair's barrier)
-        const long long t0 = clock64(), drain = ok ? kWaitCycles : kDrainCycles;
+        const long long t0 = clock64(), drain = ok && p.wait_cycles > kDrainCycles ? p.wait_cycles : kDrainCycles;
         for (int i = c > S ? c - S : 0; i < c; ++i)
             while (!test_wait_cluster(&empty[i % S], (uint32_t)((i / S) & 1)) && clock64() - t0 < drain) {
             }
@@ -267,11 +269,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             const int kb_total = p.w[at.work].kb_total(), b = q & 1;
             const uint32_t id = a_mn ? idesc_dense<I8>(2 * kTileM, BN, true, B_MN) : idesc_dense<I8>(2 * kTileM, BN, false, B_MN);
             const uint64_t step = a_mn ? 2048 >> 4 : 32 >> 4;
-            if (q >= 2 && !wait_cluster(&acc_empty[b], (uint32_t)(((q >> 1) - 1) & 1), &abort_flag)) break;
+            if (q >= 2 && !wait_cluster(&acc_empty[b], (uint32_t)(((q >> 1) - 1) & 1), &abort_flag, p.wait_cycles)) break;
             tc_fence_after();
             for (int kb = 0; kb < kb_total; ++kb, ++c) {
                 const int s = c % S;
-                if (!wait_cluster(&full[s], (uint32_t)((c / S) & 1), &abort_flag)) {
+                if (!wait_cluster(&full[s], (uint32_t)((c / S) & 1), &abort_flag, p.wait_cycles)) {
                     ok = false;
                     break;
                 }
@@ -301,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         for (TileWalk at(p, pair, pairs); at.next(); ++q) {
             const TcWork &w = p.w[at.work];
             const int b = q & 1;
-            if (!warp_wait_abort(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag, kWaitCycles)) break;
+            if (!warp_wait_abort(&acc_full[b], (uint32_t)((q >> 1) & 1), &abort_flag, p.wait_cycles)) break;
             tc_fence_after();
             const long long m0 = (long long)at.m * 2 * kTileM + rank * kTileM + quad * 32, n0 = (long long)at.n * kOutN;
             const int rows = (int)min(32LL, w.M - m0);
@@ -423,6 +425,7 @@ cudaError_t launch_t(const Product *ps, int n, int sms, cudaStream_t s) {
         tiles += a.w[1].tiles();
         a.extra = a.w[0].kb_total() / a.w[1].kb_total();
     }
+    a.wait_cycles = wait_cycles();
     e = status_word(&a.status);
     if (e != cudaSuccess) return e;
     const auto kernel = product_tc_kernel<I8, B_MN, EPI, BN, O>;
@@ -474,6 +477,19 @@ cudaError_t status_word(uint32_t **p) {
         if (dev < 64) at[dev] = *p;
     }
     return e;
+}
+
+namespace {
+std::atomic<long long> g_wait_cycles{0};   // 0: not read yet
+}
+void read_wait_cycles() {
+    const char *e = std::getenv("MOEQ_TEST_WAIT_CYCLES");
+    const long long v = e ? std::atoll(e) : 0;
+    g_wait_cycles.store(v > 0 ? v : kWaitCycles, std::memory_order_relaxed);
+}
+long long wait_cycles() {
+    if (!g_wait_cycles.load(std::memory_order_relaxed)) read_wait_cycles();
+    return g_wait_cycles.load(std::memory_order_relaxed);
 }
 
 cudaError_t sm_count(int *n) {

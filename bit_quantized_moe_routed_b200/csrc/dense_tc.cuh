@@ -15,6 +15,11 @@ namespace dense {
 constexpr int kRowBytes = 128;                  // bytes of K (or of 64 bf16 rows) a shared-memory row holds
 constexpr long long kWaitCycles = 2000000000LL; // limit of every wait between roles: about a second
 
+// The limit that a launch gives its kernel: kWaitCycles, or MOEQ_TEST_WAIT_CYCLES
+// of the environment, read at the first call and when the status word is cleared
+// (tests let a wait run out that way).
+long long wait_cycles();
+
 // Tensor map over a rows x cols matrix (row stride ld, elements of es bytes),
 // 128-byte swizzle, boxes of box_rows x 128 bytes; reads outside give zeros.
 // The base and the row stride are multiples of 16 bytes.
@@ -53,19 +58,18 @@ __device__ __forceinline__ bool test_wait_cluster(uint64_t *bar, uint32_t parity
     return ok != 0;
 }
 // Bounded wait that also ends when another role of the CTA has given up.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, long long max_cycles) {
     if (test_wait_cluster(bar, parity)) return true;
     const long long t0 = clock64();
     while (!test_wait_cluster(bar, parity)) {
         if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > max_cycles) {
             *abort_flag = 1;
             return false;
         }
     }
     return true;
 }
-
 // mbar_wait_abort by a whole warp: it gives up as one, as the tensor memory
 // loads that follow are instructions of the warp.
 __device__ __forceinline__ bool warp_wait_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag, long long max_cycles) {

@@ -155,6 +155,8 @@ cudaError_t status_word(uint32_t **p) {
     return cudaSuccess;
 }
 
+void read_wait_cycles() {}
+
 }  // namespace dense
 }  // namespace moeq
 
