@@ -234,7 +234,25 @@ def glu(x, w_gate, w_up, save=False, out=None, gu=None, workspace=None, stream=N
     """moeq_glu: h = silu(x w_gate^T) * (x w_up^T), [T][N], for x [T][H] and
     weights [N][H] (float32 or bfloat16, unit column stride).  With ``save``
     (or a ``gu`` buffer [2][T][N]) returns (h, gu) with both projections kept
-    for glu_backward."""
+    for glu_backward.
+
+    torch's autograd does not see this call (nor any other of this module): h
+    is detached, whatever x and the weights require, and no gradient flows
+    through it by itself.  To train through it, call glu and glu_backward from
+    a torch.autograd.Function::
+
+        class Glu(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, w_gate, w_up):
+                h, gu = moeq.glu(x, w_gate, w_up, save=True)
+                ctx.save_for_backward(x, w_gate, w_up, gu)
+                return h
+
+            @staticmethod
+            def backward(ctx, dh):
+                x, w_gate, w_up, gu = ctx.saved_tensors
+                return moeq.glu_backward(dh.contiguous(), x, w_gate, w_up, gu=gu)
+    """
     if stream is not None:
         with _on(x, stream, "glu"):
             return _calls.glu(x, w_gate, w_up, save, out, gu, workspace)
