@@ -204,7 +204,12 @@ bool glu_args_ok(const moeq_glu_args *a, bool backward) {
 //     45.0, 60.0; 4096 x 11008 125, 170
 //   4 tokens, kept  1024 x 1024 15.2, 13.4; 4096 x 2048 32.9, 32.4; 4096 x 4096 58.2, 45.4
 //   4 tokens, recomputed  4096 x 2048 29.2, 40.4; 4096 x 4096 60.7, 60.8; 4096 x 11008 186, 159
-// so at any size for 2 tokens, up to 2^23 for 4, whether the projections are kept or not.
+// so at any size for 2 tokens, for 4 up to 2^23 (kept) or 2^24.
+//   few columns of dx and long sums, 1 token, kept  1024 x 4096 26.3, 22.1 (weights in L2:
+//     12.0, 21.5); 512 x 8192 41, 27; 64 x 65536 264, 115; recomputed  512 x 8192 33, 45;
+//     256 x 16384 53, 58; 128 x 32768 97, 92; 64 x 65536 185, 157
+// so up to inter = 4 hidden, or 64 hidden where the projections were just computed and
+// the weights lie in L2; small ones (64 x 8192 36, 22; in L2 16, 22) in f32 all the same.
 //   rows off 16 bytes, 1 token  kept 77 x 69 6.8, 8.5; 99 x 130 11.7, 8.6; 255 x 255 13.4,
 //     9.5; 576 x 640 20.7, 15.0; recomputed 77 x 69 9.8, 12.6; 255 x 255 16.4, 14.4; 1000 x
 //     517 26.0, 17.3; 4096 x 2048 111, 66
@@ -217,7 +222,9 @@ bool few_tokens(const moeq_glu_args *a) {
     const bool aligned = rows16(a->x, a->ldx) && rows16(a->w[0], a->ldw[0]) && rows16(a->w[1], a->ldw[1]);
     const long long size = (long long)a->hidden * a->inter;
     if (!aligned) return size <= 1 << 16;
-    return a->n_tokens <= 2 || size <= 1 << 23;
+    const bool kept = a->gu != nullptr;
+    return size <= 1 << 19 ||
+           (a->inter <= (kept ? 4LL : 64LL) * a->hidden && (a->n_tokens <= 2 || size <= (kept ? 1 << 23 : 1 << 24)));
 }
 
 Plan plan_glu(const moeq_glu_args *a, bool backward) {

@@ -43,7 +43,7 @@ def plan(tmp_path_factory):
 
 SIZES = [(1, 1), (64, 138), (256, 256), (257, 256), (77, 301), (333, 260), (1000, 517), (1024, 512), (1024, 520),
          (1024, 1024), (4096, 1024), (4096, 2048), (4096, 2056), (4096, 4096), (4096, 8192), (4096, 8200), (4096, 11008),
-         (8192, 28672)]
+         (8192, 28672), (1024, 4104), (1024, 4096), (512, 8192), (128, 8192), (120, 8192), (64, 8192), (64, 65536), (4096, 4104)]
 
 
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 16, 17, 64, 1000])
@@ -69,8 +69,9 @@ def test_quantiser_grid_covers_its_rows(tmp_path):
 @pytest.mark.parametrize("T,H,I,off,dtype,kept,want", [
     # bf16 gate gradients [2][T][I padded to 64]: in f32 for few tokens
     (1, 4096, 11008, 0, 1, 0, 2 * 11008 * 4), (1, 4096, 11008, 0, 1, 1, 2 * 11008 * 4),
-    (4, 4096, 2048, 0, 1, 0, 2 * 4 * 2048 * 4), (4, 4096, 2056, 0, 1, 0, 2 * 4 * 2112 * 2),
+    (4, 4096, 2048, 0, 1, 0, 2 * 4 * 2048 * 4), (4, 4096, 2056, 0, 1, 1, 2 * 4 * 2112 * 2), (4, 4096, 4104, 0, 1, 0, 2 * 4 * 4160 * 2),
     (3, 4096, 2056, 0, 1, 1, 2 * 3 * 2112 * 2), (5, 4096, 4096, 0, 1, 0, 2 * 5 * 4096 * 2),
+    (1, 1024, 4096, 0, 1, 1, 2 * 4096 * 4), (1, 1024, 4104, 0, 1, 1, 2 * 4160 * 2), (1, 128, 8200, 0, 1, 0, 2 * 8256 * 2),
     (2, 256, 256, 3, 1, 0, 2 * 2 * 256 * 4),
     # rows off 16 bytes: and x [T] and both W [I] in rows of 128 bytes' multiples (H = 257: 640 bytes)
     (2, 257, 256, 3, 1, 0, 2 * 640 + 2 * 256 * 640 + 2 * 2 * 256 * 2),

@@ -30,12 +30,13 @@ def workspace_of(moeq, dh, x, wg, wu, gu, outs):
 
 
 # T, H, I, pad, off: rows on 16 bytes and off them; the sizes lie on both sides of hidden * inter = 2^16, 2^19 and
-# 2^23 and of T * hidden * inter = 2^25
+# 2^23 and 2^24 (3 and 4 tokens) and of inter = 4 hidden and 64 hidden
 LIMITS = [
     (1, 4096, 11008, 0, 0), (4, 4096, 4096, 0, 0), (1, 333, 260, 1, 0), (4, 1000, 517, 3, 0), (2, 1000, 517, 3, 1),
     (2, 256, 256, 3, 0), (2, 257, 256, 3, 0), (1, 301, 217, 0, 5), (3, 1024, 512, 0, 0), (3, 1024, 520, 0, 0),
     (4, 4096, 2048, 0, 0), (4, 4096, 2056, 0, 0), (4, 4096, 2048, 5, 0), (1, 8192, 4104, 8, 8), (3, 2056, 5504, 0, 0),
-    (2, 999, 1003, 0, 0), (5, 1000, 517, 3, 0), (5, 4096, 4096, 0, 0),
+    (1, 1024, 4096, 0, 0), (1, 1024, 4104, 0, 0), (2, 128, 8192, 0, 0), (2, 120, 8192, 0, 0), (3, 64, 65536, 0, 0),
+    (4, 4096, 4104, 0, 0), (2, 999, 1003, 0, 0), (5, 1000, 517, 3, 0), (5, 4096, 4096, 0, 0),
 ]
 
 
@@ -67,8 +68,8 @@ def test_gradients_on_both_sides_of_the_limits(moeq, T, H, I, pad, off):
 @pytest.mark.parametrize("T,H,I", [(1, 1024, 1024), (1, 4096, 11008), (2, 4096, 4096), (2, 2056, 5504), (3, 1000, 4000),
                                    (4, 4096, 2048)])
 def test_kept_and_recomputed_projections_round_once(moeq, T, H, I):
-    """Rows on 16 bytes, 1 and 2 tokens at any size, 3 and 4 up to 2^23 weights: dg and du stay f32
-    with the projections kept as well as without them."""
+    """Rows on 16 bytes, inter up to 4 hidden, 1 and 2 tokens at any size, 3 and 4 up to 2^23 weights: dg and du
+    stay f32 with the projections kept as well as without them."""
     torch = torch_mod()
     x, dh = mat(T, H, "bf16", 111), mat(T, I, "bf16", 114, scale=0.1)
     wg, wu = mat(I, H, "bf16", 112, scale=1.3 / H ** 0.5), mat(I, H, "bf16", 113, scale=1.3 / H ** 0.5)
