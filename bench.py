@@ -44,7 +44,7 @@ NCU_TRAFFIC = {
                       "bit_quantized_moe_routed_b200/csrc/decode_common.cuh",
                       "bit_quantized_moe_routed_b200/csrc/internal.cuh",
                       "include/moeq.h"),
-                     "7805bceb51b9e4b1201e42fe5ada0b7f052e0c72dcdaed1cadcd6a721c12efe6",
+                     "ba44cebfcb9f1d9bd422e06a6f5be7969a253fceded705160b4fc5acec012a6d",
                      107049216.0 + 358144.0, "profiles/dec_fused_mx_decode_mxfp4.md"),
 }
 

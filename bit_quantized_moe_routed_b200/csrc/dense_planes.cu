@@ -1,10 +1,10 @@
 // dense_planes.cu -- f32 products of the dense operators on the tensor cores,
 // from bf16 planes: x = hi + mid + lo, each part the nearest bf16 of what is
-// left (8 significand bits a part, so the three hold all 24 bits of an f32 in
-// the normal range).
+// left (8 significand bits a part; a bf16's smallest step is 2^-133, so the three
+// hold all 24 bits of an f32 of 2^-110 and above).
 //
 // Mathematics: x w ~ hi hi + (hi mid + mid hi + hi lo + lo hi + mid mid); the
-// products left out are below 2^-25 of |x w|.  The tensor core adds in f32 with
+// products left out are below 2^-24 of |x w| (2^-27.5 rms).  The tensor core adds in f32 with
 // truncation, which in a long sum loses about 2^-24 of the running value a
 // step of 16 products, always towards zero (measured on sums of normal values:
 // 9e-8 relative after 64 products, 6e-7 after 512, 4.8e-6 after 4096).  So the

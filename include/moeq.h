@@ -438,12 +438,16 @@ typedef struct {
 /* h[t] = silu(W_gate x[t]) * (W_up x[t]): both projections (f32 sums), the
  * activation and the product in one pass, rounded once to dtype.  With gu,
  * the two projections are also written, rounded to dtype, for a backward
- * pass.  f32 operands are multiplied in parts of 11 significand bits (three
- * products of parts, off by at most 2^-19 of a product's magnitude in sum and
- * about 2^-24 on average); an infinity among them may come out as NaN, and
- * parts below 2^-126 may count as zero.  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.  Errors:
- * INVALID_ARGUMENT (NULL, sizes, strides, unknown dtype, misaligned elements,
- * overlap, a workspace that is too small or misaligned), CUDA. */
+ * pass.  f32 operands are multiplied as three bf16 parts of 8 significand bits
+ * each, in six products of parts: what is left out is below 2^-24 of a
+ * product's magnitude, and sums are joined in f32 every 128 products.  Parts
+ * end at 2^-133, so that operands below 2^-110 keep fewer than 24 bits; an
+ * infinity among the operands may come out as NaN.  bf16 sums are the tensor
+ * cores' f32, which cut off about 2^-24 of the running value every 16 products:
+ * beside the result's rounding this shows only in sums of one sign of some 10^5
+ * products and more.  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.
+ * Errors: INVALID_ARGUMENT (NULL, sizes, strides, unknown dtype, misaligned
+ * elements, overlap, a workspace that is too small or misaligned), CUDA. */
 MOEQ_API moeq_status moeq_glu(const moeq_glu_args *a, void *stream);
 
 /* The gradients of moeq_glu for the gradient dh of its result.  With g, u the
@@ -451,11 +455,12 @@ MOEQ_API moeq_status moeq_glu(const moeq_glu_args *a, void *stream);
  *     dg = dh u s (1 + g (1 - s)),   du = dh g s
  *     dx = dg W_gate + du W_up,   dW_gate = dg^T x,   dW_up = du^T x
  * g and u are read from gu where it is given (as moeq_glu wrote it), else
- * computed again from x and w.  dg and du are rounded to dtype (they are the
- * operands of the products that follow; up to 4 tokens may keep them f32); sums are f32, rounded once.  Outputs
- * are overwritten; dx NULL or both dw NULL leaves that gradient out (not
- * both).  Reads x, w, gu, dh; h is not read.  n_tokens == 0 sets dw to zero.
- * Errors: as moeq_glu. */
+ * computed again from x and w.  dg and du are rounded to dtype, as the operands
+ * of the products that follow (up to 4 tokens may keep them f32, by sizes and
+ * alignment); sums as in moeq_glu, rounded once.  Outputs are overwritten; dx
+ * NULL or both dw NULL leaves that gradient out (not both) and does not change
+ * the other.  Reads x, w, gu, dh; h is not read.  n_tokens == 0 sets dw to
+ * zero.  Errors: as moeq_glu. */
 MOEQ_API moeq_status moeq_glu_backward(const moeq_glu_args *a, void *stream);
 
 /* Bytes of workspace that a call with these arguments needs (workspace and
