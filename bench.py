@@ -10,7 +10,8 @@ inter 2048, 256 experts, top-8).  Every rank runs its own replica on its own
 tokens (the path partitions by batch; no collective on the data path), so
 ``value`` is the total over ranks and ``scaling`` is "weak".
 
-Rank 0 prints one JSON line.  ``--impl reference`` times the oracle (the f64
+Rank 0 prints one JSON line, with the other workloads' values in short; their
+whole entries go to stderr.  ``--impl reference`` times the oracle (the f64
 CPU restatement) on the host cores instead, on a bounded sample per step.
 """
 from __future__ import annotations
@@ -643,6 +644,19 @@ def summarize(args, workload, r, world, steps, warmup, peaks, peak_src):
     return line
 
 
+def brief(res):
+    """An extra workload's entry in the printed line: what it measured, not how.  The whole entries go to stderr: with
+    them the line is 20 KB, longer than what is kept of a run's output."""
+    short = {k: res[k] for k in ("workload", "error", "value", "unit", "ms_per_step") if k in res}
+    if res.get("device_status"):
+        short["device_status"] = res["device_status"]
+    if short.get("unit") == "tokens/s":     # the line's own
+        del short["unit"]
+    if isinstance(res.get("roofline"), dict):
+        short["frac"] = res["roofline"].get("frac")
+    return {k: float(f"{v:.4g}") if isinstance(v, float) else v for k, v in short.items()}
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -718,7 +732,8 @@ def main():
 
     if rank == 0:
         if extra:
-            line["workloads"] = extra
+            line["workloads"] = {name: brief(res) for name, res in extra.items()}
+            print(json.dumps({"workloads": extra}), file=sys.stderr, flush=True)
         print(json.dumps(line), flush=True)
     if world > 1:
         dist.barrier()

@@ -75,6 +75,22 @@ def test_gather_roofline_of_the_vq_decode_kernels():
     assert g0["per_launch_bytes"] * 2 == g["per_launch_bytes"]
 
 
+def test_extra_workloads_are_short_in_the_line():
+    import json
+
+    import bench
+    whole = {"value": 13670.963476662, "unit": "tokens/s", "steps": 30, "ms_per_step": 0.0731477340062, "dtype": "bf16",
+             "config": {"workload": "decode_vq_t1", "hidden": 4096}, "roofline": {"bound": "hbm", "frac": 0.14129529, "peak": 1.0},
+             "phase_ms": {"route": 0.1}, "e2e": {"value": 9512.1865377, "unit": "tokens/s"}, "device_status": 0}
+    assert bench.brief(whole) == {"value": 13670.0, "ms_per_step": 0.07315, "frac": 0.1413}
+    assert bench.brief(dict(whole, unit="weights/s"))["unit"] == "weights/s"
+    assert bench.brief({"error": "RuntimeError: x"}) == {"error": "RuntimeError: x"}
+    assert bench.brief(dict(whole, device_status=7))["device_status"] == 7
+    # all of them within 1.1 KB: the whole line is below 3
+    names = list(bench.EXTRA_WORKLOADS) + ["router_t1", "router_t2048", "vq_encode_expert"]
+    assert len(json.dumps({n: bench.brief(whole) for n in names})) < 1100
+
+
 def test_a_failing_extra_workload_keeps_the_headline_line(monkeypatch, capsys):
     # main() with the GPU-facing steps stubbed: one extra workload raises,
     # the JSON line still prints, with the error in that workload's entry
