@@ -41,6 +41,17 @@ void check(int code, const char *name) {
     if (code != MOEQ_OK) throw Refused{code, std::string("moeq_") + name};
 }
 
+// Calls an entry point without the interpreter's lock, as ctypes does: a launch
+// waits while the device's queue is full, possibly behind a host function that
+// needs the lock.
+template <typename F, typename... A>
+int launch(F f, A... args) {
+    PyThreadState *const state = PyEval_SaveThread();
+    const int code = f(args...);   // a C function: throws nothing
+    PyEval_RestoreThread(state);
+    return code;
+}
+
 std::string describe(const at::Tensor &t) {
     std::string s = c10::toString(t.scalar_type());
     s += " (";
@@ -173,10 +184,10 @@ PyObject *quant_i8(PyObject *, PyObject *const *a, Py_ssize_t n) {
             q = c.tensor(a[1], "q");
         }
         scale = a[2] == Py_None ? c.empty({M}, at::kFloat) : c.tensor(a[2], "scale");
-        check(f_quant_i8(x.data_ptr(), act, small(M, c), small(K, c), c.ld(x, M, K, x.scalar_type(), "x"),
-                         static_cast<int8_t *>(q.data_ptr()), c.ld(q, M, K, at::kChar, "q"),
-                         const_cast<float *>(c.vec(scale, M, "scale")), c.stream),
-              c.name);
+        const int rows = small(M, c), cols = small(K, c);
+        const int64_t ldx = c.ld(x, M, K, x.scalar_type(), "x"), ldq = c.ld(q, M, K, at::kChar, "q");
+        float *const s = const_cast<float *>(c.vec(scale, M, "scale"));
+        check(launch(f_quant_i8, x.data_ptr(), act, rows, cols, ldx, static_cast<int8_t *>(q.data_ptr()), ldq, s, c.stream), c.name);
         return tuple({wrap(q), wrap(scale)});
     });
 }
@@ -206,7 +217,7 @@ PyObject *product_i8(const char *name, int nw, PyObject *xo, PyObject *xs, PyObj
         g.out = out.data_ptr();
         g.ldo = c.ld(out, T, N, out.scalar_type(), "out");
         const at::Tensor held = c.workspace(ws, f_i8_workspace(&g, nw), g.workspace, g.workspace_bytes);
-        check((nw == 1 ? f_matmul_i8 : f_glu_i8)(&g, c.stream), name);
+        check(launch(nw == 1 ? f_matmul_i8 : f_glu_i8, &g, c.stream), name);
         return wrap(out);
     });
 }
@@ -267,7 +278,7 @@ PyObject *glu(PyObject *, PyObject *const *a, Py_ssize_t n) {
         g.h = out.data_ptr();
         g.ldh = c.ld(out, g.n_tokens, g.inter, dt, "out");
         const at::Tensor held = c.workspace(a[6], f_glu_workspace(&g, 0), g.workspace, g.workspace_bytes);
-        check(f_glu(&g, c.stream), c.name);
+        check(launch(f_glu, &g, c.stream), c.name);
         return gu.defined() ? tuple({wrap(out), wrap(gu)}) : wrap(out);
     });
 }
@@ -302,7 +313,7 @@ PyObject *glu_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
             g.lddw[i] = c.ld(dw[i], I, H, dt, "dw");
         }
         const at::Tensor held = c.workspace(a[10], f_glu_workspace(&g, 1), g.workspace, g.workspace_bytes);
-        check(f_glu_backward(&g, c.stream), c.name);
+        check(launch(f_glu_backward, &g, c.stream), c.name);
         return tuple({need_dx ? wrap(dx) : none(), need_dw ? wrap(dw[0]) : none(), need_dw ? wrap(dw[1]) : none()});
     });
 }
