@@ -68,7 +68,10 @@ struct Call {
     explicit Call(const char *n) : name(n) {}
     const at::Tensor &tensor(PyObject *o, const char *what) const {
         if (!THPVariable_Check(o)) refuse(name, std::string(what) + " is not a tensor");
-        return THPVariable_Unpack(o);
+        const at::Tensor &t = THPVariable_Unpack(o);
+        // a view whose values are its memory's with the sign turned (the imaginary part of a conjugate)
+        if (t.is_neg()) refuse(name, std::string(what) + ": the negative bit is set (resolve_neg() first)");
+        return t;
     }
     // the call's device is that of its first tensor; its stream the current one there
     const at::Tensor &first(PyObject *o, const char *what) {

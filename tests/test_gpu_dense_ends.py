@@ -1,8 +1,9 @@
-"""The dense operators at the ends of their ranges: the largest number of rows."""
+"""The dense operators at the ends of their ranges: the largest numbers of rows, tokens, hidden and inter, the smallest
+values, tensors that are not what their memory holds."""
 import pytest
 
 from _gpu_util import torch_mod
-from test_gpu_dense import moeq  # noqa: F401  (the fixture)
+from test_gpu_dense import mat, moeq  # noqa: F401  (moeq: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,18 @@ def test_silu_falls_off_gradually(moeq, dtype, T):
         # dg and du may be rounded to the type once more on the way
         close(dwg[:, 0], s * (1 + g * (1 - s)), "dwg", 2.0 ** -132)
         close(dwu[:, 1], g * s, "dwu", 2.0 ** -132)
+
+
+def test_tensors_with_the_negative_bit_are_refused(moeq):
+    """Their memory holds the values with the sign turned."""
+    torch = torch_mod()
+    x, w = mat(4, 64, "bf16", 1), mat(32, 64, "bf16", 2)
+    dh = mat(4, 32, "bf16", 3)
+    n = torch._neg_view
+    q, s = moeq.quant_i8(w)
+    for call in (lambda: moeq.quant_i8(n(x)), lambda: moeq.glu(n(x), w, w), lambda: moeq.glu(x, w, n(w)),
+                 lambda: moeq.glu(x, w, w, out=n(dh)), lambda: moeq.glu_backward(n(dh), x, w, w),
+                 lambda: moeq.matmul_i8(q, n(s), q, s), lambda: moeq.matmul_i8(q, s, q, n(s))):
+        with pytest.raises(moeq.MoeqError):
+            call()
+    assert torch.equal(moeq.glu(n(x).resolve_neg(), w, w), moeq.glu(-x, w, w))
