@@ -45,7 +45,7 @@ NCU_TRAFFIC = {
                       "bit_quantized_moe_routed_b200/csrc/decode_common.cuh",
                       "bit_quantized_moe_routed_b200/csrc/internal.cuh",
                       "include/moeq.h"),
-                     "ba44cebfcb9f1d9bd422e06a6f5be7969a253fceded705160b4fc5acec012a6d",
+                     "6c178c0a1c517f47a64d7412bc6163009a848a96bf5960513f0f064e7a17976c",
                      107049216.0 + 358144.0, "profiles/dec_fused_mx_decode_mxfp4.md"),
 }
 

@@ -444,8 +444,9 @@ typedef struct {
  * end at 2^-133, so that operands below 2^-110 keep fewer than 24 bits; an
  * infinity among the operands may come out as NaN.  bf16 sums are the tensor
  * cores' f32, which cut off about 2^-24 of the running value every 16 products:
- * beside the result's rounding this shows only in sums of one sign of some 10^5
- * products and more.  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.
+ * beside the result's rounding this shows in sums of some 10^6 products and
+ * more (of the f32 ones' smaller parts too: 3e-5 of a sum over 2^24 tokens, 5e-6
+ * over 2^20, 3e-7 over a few thousand).  Reads x, w; writes h, gu.  n_tokens == 0 is a no-op.
  * Errors: INVALID_ARGUMENT (NULL, sizes, strides, unknown dtype, misaligned
  * elements, overlap, a workspace that is too small or misaligned), CUDA. */
 MOEQ_API moeq_status moeq_glu(const moeq_glu_args *a, void *stream);

@@ -3,7 +3,8 @@ values, tensors that are not what their memory holds."""
 import pytest
 
 from _gpu_util import torch_mod
-from test_gpu_dense import mat, moeq  # noqa: F401  (moeq: the fixture)
+from test_gpu_dense import (EPS, MISC, backward_refs, check, int_sum, mat, moeq, projections,  # noqa: F401  (moeq: the
+                            sigmoid)                                                           # fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,50 @@ def test_tensors_with_the_negative_bit_are_refused(moeq):
         with pytest.raises(moeq.MoeqError):
             call()
     assert torch.equal(moeq.glu(n(x).resolve_neg(), w, w), moeq.glu(-x, w, w))
+
+
+MOST = 1 << 20     # hidden and inter
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,I", [(1, MOST, 3), (4, MOST, 2), (16, MOST, 5), (40, MOST, 3), (300, MOST - 1, 2), (1, 5, MOST),
+                                   (4, 8, MOST), (16, 3, MOST), (40, 8, MOST - 3), (300, 2, MOST), ((1 << 24) + 3, 8, 8),
+                                   ((1 << 22) + 1, 3, 17)])
+def test_the_largest_sizes(moeq, T, H, I, dtype):
+    """Element by element within bounds that grow with the sums' length, and in the norm within what the errors leave
+    of them together: bf16 rounds a result and a gate gradient by at most 2^-8 / sqrt(3) each; a tensor-core step of 16
+    products cuts off up to 2^-24 of the running value on average, in the projections and in the gradients' sums.  f32:
+    1e-6 for sums of 4096 (test_gpu_dense_f32.py), the joins of pieces of 128 by 2^-25 each and independently, the five
+    small products below 2^-8 of that cut-off; three sums behind one another."""
+    torch = torch_mod()
+    x, dh = mat(T, H, dtype, 1), mat(T, I, dtype, 2, scale=0.1)
+    wg, wu = mat(I, H, dtype, 3, scale=1.3 / H ** 0.5), mat(I, H, dtype, 4, scale=1.3 / H ** 0.5)
+    g, u, eg, eu = projections(x, wg, wu)
+    h, gu = moeq.glu(x, wg, wu, save=True)
+    ref = g * sigmoid(g) * u
+    hb = 1.1 * eg * (u.abs() + eu) + (g * sigmoid(g)).abs() * eu
+    check(h, ref, hb + (ref.abs() + hb) * (MISC + EPS[dtype] * 1.001), "h")
+    del ref, hb, h
+    zero = torch.zeros_like(g)
+    L = max(T, H, 2 * I)
+    near = {"bf16": 3.2e-3 + 2 * L / 16 * 2.0 ** -24,
+            "f32": 3 * (1e-6 + (L / 128) ** 0.5 * 2.0 ** -25 + 5 * L / 16 * 2.0 ** -32)}[dtype]
+    for kept, pr in ((gu, (gu[0].double(), gu[1].double(), zero, zero)), (None, (g, u, eg, eu))):
+        got = moeq.glu_backward(dh, x, wg, wu, gu=kept)
+        for o, (want, bound), what in zip(got, backward_refs(dh, x, wg, wu, *pr, dtype), ("dx", "dwg", "dwu")):
+            check(o, want, bound, what + (" (kept)" if kept is not None else ""))
+            e = ((o.double() - want).norm() / want.norm()).item()
+            assert e <= near, (what, e)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 131071, 5), (16, 131071, 3), (40, 131071, 2), (300, 131071, 2), (1, 5, MOST), (16, 3, MOST),
+                                   (40, 17, MOST), (300, 16, MOST - 1), ((1 << 24) + 3, 16, 5)])
+def test_the_largest_int8_sizes(moeq, T, K, N):
+    torch = torch_mod()
+    x, w = mat(T, K, "i8", 1), mat(N, K, "i8", 2)
+    sx, sw = (torch.rand(n, device="cuda") * 1e-2 + 1e-4 for n in (T, N))
+    out = moeq.matmul_i8(x, sx, w, sw, dtype="f32")
+    step = max(1, (1 << 26) // N)
+    for t in range(0, T, step):
+        ref = int_sum(x[t:t + step], w) * sx[t:t + step].double()[:, None] * sw.double()
+        check(out[t:t + step], ref, ref.abs() * 3.01 * 2.0 ** -24, "matmul_i8")
