@@ -121,3 +121,15 @@ def test_the_largest_int8_sizes(moeq, T, K, N):
     for t in range(0, T, step):
         ref = int_sum(x[t:t + step], w) * sx[t:t + step].double()[:, None] * sw.double()
         check(out[t:t + step], ref, ref.abs() * 3.01 * 2.0 ** -24, "matmul_i8")
+
+
+def test_no_tokens_and_rows_far_apart(moeq):
+    """dW of no tokens is zero, with rows 2 GB and more apart too; what lies between them stays."""
+    torch = torch_mod()
+    ld = (1 << 30) + 64
+    buf = torch.full((2 * ld + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    dwg, dwu = buf.as_strided((3, 64), (ld, 1)), buf.as_strided((3, 64), (ld, 1), 64)
+    w = mat(3, 64, "bf16", 1)
+    moeq.glu_backward(mat(0, 3, "bf16", 2), mat(0, 64, "bf16", 3), w, w, dw_gate=dwg, dw_up=dwu, need_dx=False)
+    assert not dwg.any() and not dwu.any()
+    assert all(bool((buf[i * ld + 128:(i + 1) * ld] == 7).all()) for i in range(2))
